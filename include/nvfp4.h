@@ -400,6 +400,116 @@ int nvfp4_set_decode_wait_test(int withhold, int spin_limit);
  * value, or NVFP4_ERR_INVALID_ARG. */
 int nvfp4_set_path(int path);
 
+/*
+ * ---- The attention half of a decoder layer ----
+ *
+ * Residual addition + root-mean-square norm + NVFP4 quantization, in front of
+ * nvfp4_gemm or gemm_swiglu_nvfp4_quant. Per row of K elements:
+ *   z = x + residual in fp32, rounded to the residual's type (z = x if
+ *   residual is NULL);  ms = sum z^2 / K in fp64;  rstd = fl(1 / sqrt(ms + eps));
+ *   y = fl(fl(z * rstd) * w);  codes, scales = y quantized with g_inv exactly
+ *   as nvfp4_quantize does an f32 tensor.
+ * The sum is exact to fp64, so the codes depend on the values alone.
+ * x [M, K] of x_dtype, residual [M, K] of residual_dtype, w [K] of w_dtype
+ * (each bf16 or f32), K % 16 == 0, at most 2^24. residual_out [M, K] receives
+ * z (residual_dtype; x_dtype if residual is NULL); it may be NULL, residual
+ * or x (the latter where both have one type). codes [M, K/2], scales [M, K/16].
+ * The per-token form calibrates each row on its own y (g = fl(max|y| / 2688),
+ * g_inv = fl(1 / g), 0 for a zero row) and writes row_g [M], as
+ * nvfp4_quantize_per_token does.
+ */
+int add_rmsnorm_nvfp4_quant(const void* x, int x_dtype, const void* residual, int residual_dtype, const void* w,
+                            int w_dtype, double eps, int64_t M, int64_t K, const float* g_inv, void* residual_out,
+                            uint8_t* codes, uint8_t* scales, void* stream);
+int add_rmsnorm_nvfp4_quant_per_token(const void* x, int x_dtype, const void* residual, int residual_dtype,
+                                      const void* w, int w_dtype, double eps, int64_t M, int64_t K, void* residual_out,
+                                      uint8_t* codes, uint8_t* scales, float* row_g, void* stream);
+
+/*
+ * The numbers an NVFP4 tensor stands for: out[m, k] = fl(E2M1 * E4M3 * g),
+ * rounded to out_dtype. codes [M, K/2], scales [M, K/16], K % 16 == 0; exactly
+ * one of g (1-element device fp32) and row_g (device fp32 [M]) is given.
+ */
+int nvfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, const float* g,
+                     const float* row_g, void* out, int out_dtype, void* stream);
+
+/*
+ * Paged NVFP4 cache of one layer's keys and values: `pages` pages of
+ * page_size tokens (a multiple of 16, at most 65536) of `heads` heads of
+ * head_dim channels (64, 128 or 256). A slot is page * page_size + the
+ * token's place in its page. Keys and values are quantized in blocks of 16
+ * channels; 9/8 byte per (token, head, channel) for both together. Layout:
+ * uint8 [pages, heads, page_size / 16, 18 * head_dim], a record per 16 tokens
+ * of one head, D = head_dim, g = 0..3, b = 0..D/16 - 1:
+ *   K codes  [4 g][16 t][D/8]       token t, channels g D/4 + [0, D/4), two
+ *                                   per byte, low nibble first
+ *   V codes  [4 g][16 c][D/16 b][2] channel 16 b + c, tokens 4 g + {0, 1} and
+ *                                   4 g + {2, 3}, low nibble first
+ *   K scales [4 g][16 t][D/64]      blocks g D/64 + [0, D/64) of token t
+ *   V scales [4 g][D/16 b][4]       block b of tokens 4 g + [0, 4)
+ * The caller owns it; it needs no initial contents. nvfp4_kv_cache_bytes is
+ * its size, 0 for invalid arguments.
+ */
+size_t nvfp4_kv_cache_bytes(int64_t pages, int64_t page_size, int64_t heads, int64_t head_dim);
+
+/*
+ * Quantizes k and v [T, heads, head_dim] (bf16 or f32, token strides in
+ * elements, multiples of 16 bytes, heads and channels dense, so slices of a
+ * projection's output pass as they are) as nvfp4_quantize does with k_g_inv
+ * and v_g_inv (1-element device fp32) and stores token t at slots[t] (device
+ * int64). Slots outside the cache (negative: padding) are skipped. No slot
+ * may be named twice in one call: what it then holds is unspecified. Other
+ * tokens' bits are untouched.
+ */
+int nvfp4_kv_write(const void* k, const void* v, int dtype, int64_t T, int64_t k_stride, int64_t v_stride,
+                   const int64_t* slots, const float* k_g_inv, const float* v_g_inv, void* cache, int64_t pages,
+                   int64_t page_size, int64_t heads, int64_t head_dim, void* stream);
+
+/*
+ * The numbers the cache holds at slots[t], as nvfp4_dequantize gives them, to
+ * dense k and v [T, heads, head_dim] of dtype; zeros for slots outside the
+ * cache. A slot may be named any number of times.
+ */
+int nvfp4_kv_read(const void* cache, int64_t pages, int64_t page_size, int64_t heads, int64_t head_dim,
+                  const int64_t* slots, int64_t T, const float* k_g, const float* v_g, void* k, void* v, int dtype,
+                  void* stream);
+
+/*
+ * Causal attention over the cache. Sequence b of B has seq_lens[b] keys
+ * (device int32), key j at page block_table[b * table_stride + j / page_size]
+ * (device int32 [B, table_width]); its queries are the rows q_offsets[b] ..
+ * q_offsets[b + 1] of q [T, heads_q, head_dim] (device int32 [B + 1]; NULL:
+ * max_q each, T = B * max_q) and stand at its last positions, query i of n at
+ * p = seq_lens[b] - n + i. It sees the keys max(0, p - window + 1) .. p
+ * (window 0: 0 .. p); query head a reads kv head a / (heads_q / heads).
+ *   out = sum_j softmax_j(scale * q . k_j) v_j,  lse = log sum_j exp(scale * q . k_j)
+ * (natural logarithm, after scaling). A query that sees no key gets out = 0,
+ * lse = -inf. q is bf16 with a token stride in elements (a multiple of 8);
+ * out [T, heads_q, head_dim] of out_dtype; lse fp32 [T, heads_q] or NULL. Rows
+ * of q that belong to no sequence are not written.
+ * max_q and max_len are host-side bounds of the query counts and lengths: at
+ * most max_q queries of a sequence are computed and its length is clamped to
+ * max_len and to the table's width. Keys whose table entry is not a page of
+ * the cache are not read and count as hidden. Entries past a sequence's length
+ * are not read.
+ * Products run on the f16 matrix core with fp32 accumulation: the cache's
+ * values are exact in f16, probabilities round to 11 bits, sums and the
+ * softmax statistics are fp32. The result does not depend on the order in
+ * which workgroups finish.
+ * ws: nvfp4_kv_attention_workspace_bytes(...) bytes, 16-byte aligned. Its
+ * first 4096 bytes (arrival counters of a split key axis) must be zero the
+ * first time and are left zero by every call; calls of any sizes may share
+ * it, one at a time.
+ */
+size_t nvfp4_kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t heads_q, int64_t heads, int64_t head_dim,
+                                          int64_t max_q, int64_t max_len);
+int nvfp4_kv_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64_t B, int64_t heads_q,
+                       const int32_t* q_offsets, int64_t max_q, const void* cache, int64_t pages, int64_t page_size,
+                       int64_t heads, int64_t head_dim, const int32_t* block_table, int64_t table_stride,
+                       int64_t table_width, const int32_t* seq_lens, int64_t max_len, float scale, int64_t window,
+                       const float* k_g, const float* v_g, void* ws, size_t ws_bytes, void* out, int out_dtype,
+                       float* lse, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
