@@ -102,17 +102,24 @@ def _check(name, code):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+_gpu = False  # a GPU has been seen: it does not go away
 
 
 def _stream(stream):
+    """The stream's handle. The current one is asked for without building a Stream object (0.1 us, not 3.5)."""
+    global _gpu
     if stream is None:
-        if torch.cuda.is_available():
-            return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-        return None
+        if not _gpu:
+            if not torch.cuda.is_available():
+                return None
+            _gpu = True
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _dtype_code(dt):

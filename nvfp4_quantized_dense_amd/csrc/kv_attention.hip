@@ -46,13 +46,13 @@ __device__ __forceinline__ f16x4 e4m3x4_f16(uint32_t w) {
   return f16x4{a[0], a[1], b[0], b[1]};
 }
 
-// A lane's share of a record: the codes of its token (K) and channel (V) and
-// their scales.
+// A lane's share of a record: the codes of its token (K) and channel (V), its
+// token's K scales, and the V scales of block lane % (D / 16) of its quad (the
+// other blocks' are with the quad's other lanes).
 template <int D>
 struct Frag {
   static constexpr int kW = D / 32;   // code dwords
-  static constexpr int kB = D / 16;   // V scale dwords
-  uint32_t k[kW], v[kW], ks, vs[kB];
+  uint32_t k[kW], v[kW], ks, vs;
 };
 
 template <int N>
@@ -78,7 +78,36 @@ __device__ __forceinline__ void load_frag(Frag<D>& f, const uint8_t* rec, int la
   if constexpr (D == 64) f.ks = *s;
   else if constexpr (D == 128) f.ks = *reinterpret_cast<const uint16_t*>(s);
   else f.ks = *reinterpret_cast<const uint32_t*>(s);
-  load_words(f.vs, rec + R::kVs + (lane >> 4) * (D / 4));
+  f.vs = *reinterpret_cast<const uint32_t*>(rec + R::kVs + (lane >> 4) * (D / 4) + (lane & (D / 16 - 1)) * 4);
+}
+
+// Lane N's value in each row of 16 lanes.
+template <int N>
+__device__ __forceinline__ uint32_t row_bcast(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x150 + N, 0xF, 0xF, true);
+}
+
+// V^T of channel block Y as an operand: 4 tokens of each of two records.
+template <int D, int Y>
+__device__ __forceinline__ f16x8 v_operand(const Frag<D> (&f)[2], const f16x4 (&vs)[2]) {
+  f16x8 r;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const uint32_t w = f[x].v[Y >> 1];
+    const u32x2 s = __builtin_bit_cast(u32x2, vs[x]);
+    const f16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2 * (Y & 1)) * __builtin_bit_cast(f16x2, row_bcast<Y>(s[0]));
+    const f16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2 * (Y & 1) + 1) * __builtin_bit_cast(f16x2, row_bcast<Y>(s[1]));
+    r[4 * x] = lo[0]; r[4 * x + 1] = lo[1]; r[4 * x + 2] = hi[0]; r[4 * x + 3] = hi[1];
+  }
+  return r;
+}
+
+template <int D, int RT, int Y>
+__device__ __forceinline__ void pv(f32x4 (&o)[RT][D / 16], const Frag<D> (&f)[2], const f16x4 (&vs)[2], const f16x8 (&pf)[RT]) {
+  const f16x8 vf = v_operand<D, Y>(f, vs);
+#pragma unroll
+  for (int t = 0; t < RT; ++t) o[t][Y] = mfma16x16x32(vf, pf[t], o[t][Y]);
+  if constexpr (Y + 1 < D / 16) pv<D, RT, Y + 1>(o, f, vs, pf);
 }
 
 // Keeps the bytes of the quad's tokens first .. first + 3 that lie in [lo, hi).
@@ -90,9 +119,13 @@ __device__ __forceinline__ uint32_t byte_mask(int first, int lo, int hi) {
   return m;
 }
 
+// Workgroups per CU that the registers are held to.
 template <int D, int RT>
-__global__ __launch_bounds__(256) void k_kv_attention(AttnArgs a, AttnPlan p) {
-  using R = KvRec<D>;
+constexpr int kAttnWgs = D == 256 ? 1 : RT == 2 ? 2 : D == 64 ? 4 : 3;
+
+template <int D, int RT>
+__global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArgs a, AttnPlan p) {
+#if defined(__HIP_DEVICE_COMPILE__)
   constexpr int kB = D / 16, kW = D / 32, kRows = 16 * RT;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
@@ -132,7 +165,7 @@ __global__ __launch_bounds__(256) void k_kv_attention(AttnArgs a, AttnPlan p) {
   const int active = hi_all > lo_all ? (int)((hi_all - start + p.chunk - 1) / p.chunk) : 1;
   if (split >= active) return;
 
-  float row_m[RT], row_l[RT], row_f[RT];
+  float row_m[RT], row_l[RT], row_f[RT], row_t[RT];
   int row_lo[RT], row_hi[RT];
   f16x8 qf[RT][kW];
 #pragma unroll
@@ -143,7 +176,7 @@ __global__ __launch_bounds__(256) void k_kv_attention(AttnArgs a, AttnPlan p) {
     const int head = h * G + (int)(row - i * G);
     row_hi[t] = live ? hi_of((int)i) : 0;
     row_lo[t] = live ? lo_of(row_hi[t]) : 0;
-    row_m[t] = kNoKey;
+    row_m[t] = row_t[t] = kNoKey;
     row_l[t] = 0.0f;
     uint32_t w[kW * 4];
     uint32_t top = 0;
@@ -167,8 +200,12 @@ __global__ __launch_bounds__(256) void k_kv_attention(AttnArgs a, AttnPlan p) {
     // (bounded so that both factors are normal numbers).
     int e = (int)(top >> 23) - 127;
     e = e < -100 ? -100 : (e > 126 ? 126 : e);
-    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-    row_f[t] = __uint_as_float((uint32_t)(127 + e) << 23) * (a.scale * *a.k_g) * kLog2e;
+    float down = __uint_as_float((uint32_t)(127 - e) << 23);
+    // The factor's sign goes into q, so that the largest raw score is the
+    // largest score.
+    const float f = __uint_as_float((uint32_t)(127 + e) << 23) * (a.scale * *a.k_g) * kLog2e;
+    row_f[t] = __builtin_fabsf(f);
+    if (f < 0.0f) down = -down;
 #pragma unroll
     for (int s = 0; s < kW; ++s)
 #pragma unroll
@@ -194,28 +231,33 @@ __global__ __launch_bounds__(256) void k_kv_attention(AttnArgs a, AttnPlan p) {
   const int steps = s_last > s_first ? (int)((s_last - s_first + 31) / 32) : 0, per = (steps + 3) / 4;
   const int step0 = wave * per, step1 = step0 + per < steps ? step0 + per : steps;
 
-  // The record of group g (16 tokens from 16 g); false if its page is not in
-  // the cache. Groups past the last key stand for the last key's.
-  auto record = [&](int64_t g, const uint8_t*& rec) {
-    const int64_t g_last = (hi_all - 1) >> 4;
-    g = g < g_last ? g : g_last;
-    const int64_t ps = g / groups;
-    const int page = __builtin_amdgcn_readfirstlane(table[ps]);
-    const bool ok = page >= 0 && page < a.c.pages;
-    rec = a.c.cache + rec_offset<D>(ok ? page : 0, a.c.heads, h, groups, (int)(g - ps * groups));
-    return ok;
+  // Records are taken in order: group g is group `in` of page slot `ps`,
+  // whose page number is in a lane of `tab` (64 slots from tab0 on). Groups
+  // past the last key stand for the last key's and are masked.
+  int g = (int)(s_first >> 4) + 2 * step0, ps = g / groups, in = g - ps * groups, tab0 = ps;
+  const int g_last = (hi_all - 1) >> 4, ps_last = g_last / groups;
+  int tab = 0;
+  auto load_tab = [&] {
+    const int at = tab0 + lane;
+    tab = table[at < ps_last ? at : ps_last];
   };
-
-  for (int st = step0; st < step1; ++st) {
-    const int base = (int)s_first + 32 * st;
-    Frag<D> f[2];
-    bool ok[2];
+  auto fetch = [&](Frag<D> (&f)[2], bool (&ok)[2]) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const uint8_t* rec;
-      ok[x] = record((base >> 4) + x, rec);
-      load_frag<D>(f[x], rec, lane);
+      if (ps - tab0 == 64) {
+        tab0 = ps;
+        load_tab();
+      }
+      const int page = __builtin_amdgcn_readlane(tab, ps - tab0);
+      ok[x] = page >= 0 && page < a.c.pages;
+      load_frag<D>(f[x], a.c.cache + rec_offset<D>(ok[x] ? page : 0, a.c.heads, h, groups, in), lane);
+      if (g < g_last) {
+        ++g;
+        if (++in == groups) { in = 0; ++ps; }
+      }
     }
+  };
+  auto attend = [&](Frag<D> (&f)[2], const bool (&ok)[2], int base) {
     const bool edge = base + 32 > hi_full || base < lo_full || !ok[0] || !ok[1];
     // S^T of two groups, all row tiles.
     f32x4 sc[RT][2];
@@ -231,82 +273,92 @@ __global__ __launch_bounds__(256) void k_kv_attention(AttnArgs a, AttnPlan p) {
         for (int t = 0; t < RT; ++t) sc[t][x] = mfma16x16x32(kf, qf[t][s], sc[t][x]);
       }
     }
+    uint32_t hide[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) hide[t] = 0;
     if (edge) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int first = base + 16 * x + 4 * quad;
         // Tokens no row sees may never have been written: their V scales
         // become zero, so that no NaN code meets a zero probability.
-        const uint32_t keep = ok[x] ? byte_mask(first, lo_all, hi_all) : 0u;
+        f[x].vs &= ok[x] ? byte_mask(first, lo_all, hi_all) : 0u;
 #pragma unroll
-        for (int y = 0; y < kB; ++y) f[x].vs[y] &= keep;
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (!ok[x] || first + r < row_lo[t] || first + r >= row_hi[t]) {
+              hide[t] |= 1u << (4 * x + r);
+              sc[t][x][r] = -__builtin_inff();
+            }
       }
     }
     f16x8 pf[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      float s8[8];
+      float mx = sc[t][0][0];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        s8[r] = sc[t][0][r] * row_f[t];
-        s8[4 + r] = sc[t][1][r] * row_f[t];
+      for (int r = 1; r < 8; ++r) mx = __builtin_fmaxf(mx, sc[t][r >> 2][r & 3]);
+      // The subtracted maximum follows the true one only when a score passes
+      // it by more than 2^8 in probability: f16 holds probabilities up to
+      // that as exactly as up to 1, and most steps then need neither the
+      // exchange between lanes nor the rescaling.
+      if (__any(mx > row_t[t])) {
+        mx = max_xor32(max_xor16(mx));
+        const float mn = __builtin_fmaxf(row_m[t], mx);
+        const float alpha = __builtin_amdgcn_exp2f((row_m[t] - mn) * row_f[t]);
+        row_m[t] = mn;
+        row_t[t] = mn == kNoKey ? kNoKey : mn + 8.0f / row_f[t];
+        row_l[t] *= alpha;
+#pragma unroll
+        for (int y = 0; y < kB; ++y) o[t][y] *= alpha;
       }
+      const float mf = -row_m[t] * row_f[t];
+      float e[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][r >> 2][r & 3], row_f[t], mf));
       if (edge) {
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const int tok = base + 16 * (r >> 2) + 4 * quad + (r & 3);
-          if (!ok[r >> 2] || tok < row_lo[t] || tok >= row_hi[t]) s8[r] = -__builtin_inff();
-        }
+        for (int r = 0; r < 8; ++r) e[r] = (hide[t] >> r) & 1 ? 0.0f : e[r];
       }
-      float mx = s8[0];
-#pragma unroll
-      for (int r = 1; r < 8; ++r) mx = __builtin_fmaxf(mx, s8[r]);
-      mx = max_xor32(max_xor16(mx));
-      const float mn = __builtin_fmaxf(row_m[t], mx);
-      const float alpha = __builtin_amdgcn_exp2f(row_m[t] - mn);
-      row_m[t] = mn;
-      float sum = 0.0f;
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
-        const float e = __builtin_amdgcn_exp2f(s8[r] - mn);
-        sum += e;
-        pf[t][r] = (_Float16)e;
+        row_l[t] += e[r];
+        pf[t][r] = (_Float16)e[r];
       }
-      row_l[t] = row_l[t] * alpha + sum;
-#pragma unroll
-      for (int y = 0; y < kB; ++y) o[t][y] *= alpha;
     }
     // O^T += V^T P, 16 channels at a time.
-#pragma unroll
-    for (int y = 0; y < kB; ++y) {
-      f16x8 vf;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const f16x4 s = e4m3x4_f16(f[x].vs[y]);
-        const uint32_t w = f[x].v[y >> 1];
-        f16x2 lo, hi;
-        if (y & 1) {
-          lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2);
-          hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3);
-        } else {
-          lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0);
-          hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1);
-        }
-        lo *= f16x2{s[0], s[1]};
-        hi *= f16x2{s[2], s[3]};
-        vf[4 * x] = lo[0]; vf[4 * x + 1] = lo[1]; vf[4 * x + 2] = hi[0]; vf[4 * x + 3] = hi[1];
-      }
-#pragma unroll
-      for (int t = 0; t < RT; ++t) o[t][y] = mfma16x16x32(vf, pf[t], o[t][y]);
+    const f16x4 vs[2] = {e4m3x4_f16(f[0].vs), e4m3x4_f16(f[1].vs)};
+    pv<D, RT, 0>(o, f, vs, pf);
+  };
+  if (step0 < step1) {
+    // The next step's records are on their way while one is computed.
+    Frag<D> fa[2], fb[2];
+    bool ka[2], kb[2];
+    load_tab();
+    fetch(fa, ka);
+    for (int st = step0; st < step1; st += 2) {
+      const int base = (int)s_first + 32 * st;
+      if (st + 1 < step1) fetch(fb, kb);
+      attend(fa, ka, base);
+      if (st + 1 >= step1) break;
+      if (st + 2 < step1) fetch(fa, ka);
+      attend(fb, kb, base + 32);
     }
   }
+  // From here on in units of log2.
+#pragma unroll
+  for (int t = 0; t < RT; ++t) row_l[t] = sum_xor32(sum_xor16(row_l[t]));
+#pragma unroll
+  for (int t = 0; t < RT; ++t) row_m[t] = row_m[t] == kNoKey ? kNoKey : row_m[t] * row_f[t];
 
   // The four waves' results become one: weights exp2(m_w - m) per row.
   __shared__ float wm[4][kRows], wl[4][kRows];
-  __shared__ f32x4 wo[4][kB][64];
+  constexpr int kJoin = 4096;  // (split, row) pairs that the join holds
+  __shared__ f32x4 lds[4 * kB * 64 > kJoin / 2 ? 4 * kB * 64 : kJoin / 2];
+  auto wo = [&](int w, int y) -> f32x4& { return lds[(w * kB + y) * 64 + lane]; };
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
-    row_l[t] = sum_xor32(sum_xor16(row_l[t]));
     if (quad == 0) {
       wm[wave][16 * t + col] = row_m[t];
       wl[wave][16 * t + col] = row_l[t];
@@ -316,6 +368,7 @@ __global__ __launch_bounds__(256) void k_kv_attention(AttnArgs a, AttnPlan p) {
   const float vg = *a.v_g;
   const int64_t slot = unit * p.splits + split;
   float* part = a.part + slot * (int64_t)p.part_floats;  // [kRows] m, [kRows] l, [kRows][D] o
+  const Rsrc rp = make_rsrc(part, (uint32_t)(p.part_floats * 4));
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     const int rr = 16 * t + col;
@@ -326,7 +379,7 @@ __global__ __launch_bounds__(256) void k_kv_attention(AttnArgs a, AttnPlan p) {
     for (int w = 0; w < 4; ++w) l += wl[w][rr] * __builtin_amdgcn_exp2f(wm[w][rr] - m);
     if (t > 0) __syncthreads();
 #pragma unroll
-    for (int y = 0; y < kB; ++y) wo[wave][y][lane] = o[t][y] * alpha;
+    for (int y = 0; y < kB; ++y) wo(wave, y) = o[t][y] * alpha;
     __syncthreads();
     // Wave w finishes channel blocks w, w + 4, ...: lane (quad, col) holds
     // channels 16 y + 4 quad + [0, 4) of row 16 t + col.
@@ -334,7 +387,7 @@ __global__ __launch_bounds__(256) void k_kv_attention(AttnArgs a, AttnPlan p) {
     const int64_t i = row / G;
     const int64_t orow = (q0 + i) * a.heads_q + h * G + (row - i * G);
     for (int y = wave; y < kB; y += 4) {
-      const f32x4 v = wo[0][y][lane] + wo[1][y][lane] + wo[2][y][lane] + wo[3][y][lane];
+      const f32x4 v = wo(0, y) + wo(1, y) + wo(2, y) + wo(3, y);
       if (active == 1) {
         if (row < rows) {
           const float inv = l > 0.0f || l != l ? vg / l : 0.0f;
@@ -349,10 +402,7 @@ __global__ __launch_bounds__(256) void k_kv_attention(AttnArgs a, AttnPlan p) {
           }
         }
       } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          __hip_atomic_store(part + 2 * kRows + rr * D + 16 * y + 4 * quad + e, v[e], __ATOMIC_RELAXED,
-                             __HIP_MEMORY_SCOPE_AGENT);
+if (row < rows) bstore16_dev(rp, (uint32_t)(8 * kRows + (rr * D + 16 * y + 4 * quad) * 4), __builtin_bit_cast(u32x4, v));
       }
     }
     if (wave == 0 && quad == 0) {
@@ -380,22 +430,36 @@ __global__ __launch_bounds__(256) void k_kv_attention(AttnArgs a, AttnPlan p) {
   if (arrived != (uint32_t)(active - 1)) return;
   if (threadIdx.x == 0) __hip_atomic_store(a.counters + unit, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   const float* parts = a.part + unit * p.splits * (int64_t)p.part_floats;
-  auto get = [&](int s, int64_t at) {
-    return __hip_atomic_load(parts + s * (int64_t)p.part_floats + at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  };
-  for (int n = threadIdx.x; n < kRows * (D / 4); n += 256) {
+  const Rsrc ra = make_rsrc(parts, (uint32_t)(active * p.part_floats * 4));
+  float* jm = reinterpret_cast<float*>(lds);  // [active][kRows] m, then l
+  float* jl = jm + kJoin;
+  for (int n = threadIdx.x; n < active * kRows; n += 256) {
+    const uint32_t at = (uint32_t)((n / kRows * p.part_floats + n % kRows) * 4);
+    jm[n] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(ra, (int)at, 0, 16));
+    jl[n] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(ra, (int)at, 4 * kRows, 16));
+  }
+  __syncthreads();
+  const int live = rows - row0 < kRows ? (int)(rows - row0) : kRows;
+  for (int n = threadIdx.x; n < live * (D / 4); n += 256) {
     const int rr = n / (D / 4), d = n % (D / 4) * 4;
     const int64_t row = row0 + rr;
-    if (row >= rows) continue;
     float m = kNoKey;
-    for (int s = 0; s < active; ++s) m = __builtin_fmaxf(m, get(s, rr));
+    for (int s = 0; s < active; ++s) m = __builtin_fmaxf(m, jm[s * kRows + rr]);
     float l = 0.0f;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < active; ++s) {
-      const float w = __builtin_amdgcn_exp2f(get(s, rr) - m);
-      l += w * get(s, kRows + rr);
+    const uint32_t at = (uint32_t)(8 * kRows + (rr * D + d) * 4);
+    for (int s = 0; s < active; s += 8) {
+      f32x4 x[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += w * get(s, 2 * kRows + rr * D + d + e);
+      for (int e = 0; e < 8; ++e)  // past the last split: zeros, unread
+        x[e] = __builtin_bit_cast(f32x4, bload16_dev(ra, s + e < active ? at + (uint32_t)((s + e) * p.part_floats * 4) : kOutOfRange));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (s + e >= active) break;
+        const float w = __builtin_amdgcn_exp2f(jm[(s + e) * kRows + rr] - m);
+        l += w * jl[(s + e) * kRows + rr];
+        v += x[e] * w;
+      }
     }
     const float inv = l > 0.0f || l != l ? vg / l : 0.0f;
     const f32x4 r = v * inv;
@@ -410,6 +474,7 @@ __global__ __launch_bounds__(256) void k_kv_attention(AttnArgs a, AttnPlan p) {
     }
     if (d == 0 && a.lse != nullptr) a.lse[orow] = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
   }
+#endif  // __HIP_DEVICE_COMPILE__
 }
 
 template <int D>
@@ -435,6 +500,7 @@ AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t max_q, in
   // About 1024 workgroups (4 per CU), at least 256 keys each.
   int64_t want = p.units > 0 ? (1024 + p.units - 1) / p.units : 1;
   int64_t most = (span + 255) / 256;
+  if (most > 4096 / per) most = 4096 / per;  // what the join holds
   if (want > most) want = most;
   if (want < 1) want = 1;
   int64_t bound = p.units > 0 ? (1024 + p.units - 1) / p.units : 1;
