@@ -1140,7 +1140,7 @@ static int attn_sizes(int64_t T, int64_t B, int64_t heads_q, int64_t heads, int6
   if (max_len < 0 || max_len > (int64_t(1) << 30)) return fail(NVFP4_ERR_INVALID_ARG, "max_len must be 0 to 2^30");
   if (window < 0 || window > (int64_t(1) << 30)) return fail(NVFP4_ERR_INVALID_ARG, "window must be 0 to 2^30");
   p = nvfp4::attn_plan(B, (int)heads_q, (int)heads, (int)head_dim, max_q, max_len, window);
-  if (p.units > (int64_t(1) << 23)) return fail(NVFP4_ERR_INVALID_ARG, "too many sequences, heads and queries for one call");
+  if (p.units > nvfp4::kAttnMaxUnits) return fail(NVFP4_ERR_INVALID_ARG, "too many sequences, heads and queries for one call");
   return NVFP4_OK;
 }
 
@@ -1149,7 +1149,7 @@ size_t nvfp4_kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t heads_q,
   nvfp4::AttnPlan p;
   if (attn_sizes(T, B, heads_q, heads, head_dim, max_q, max_len, 0, p)) return 0;
   size_t n = kAttnCounters * sizeof(uint32_t);
-  if (p.splits_bound > 1) n += align256((size_t)p.units * p.splits_bound * p.part_floats * sizeof(float));
+  if (p.splits_bound > 1) n += align256((size_t)p.units * p.splits_bound * (size_t)p.part_floats * sizeof(float));
   return n;
 }
 

@@ -64,17 +64,25 @@ struct AttnArgs {
   float* part;               // split partials
   uint32_t* counters;        // one per (row block, head, sequence), zero
 };
-// The split of a call, by its host-side sizes alone.
+// The split of a call, by its host-side sizes alone; units alone if there are
+// more than kAttnMaxUnits.
+constexpr int64_t kAttnMaxUnits = int64_t(1) << 23;
 struct AttnPlan {
-  int row_tiles;        // 16-row tiles per workgroup
-  int64_t row_blocks;   // per (sequence, head)
+  bool tiled;           // kv_attention_tile.hip, else kv_attention.hip
+  int row_tiles;        // 16-row tiles per workgroup, tiled: per wave
   int64_t units;        // row_blocks * B * heads
-  int64_t chunk;        // keys per split
-  int64_t splits;       // most splits of one unit
+  int row_blocks;       // per (sequence, head)
+  int chunk;            // keys per split
+  int splits;           // most splits of one unit
   int64_t splits_bound; // the same over all windows
-  size_t part_floats;   // per (unit, split)
+  int part_floats;      // per (unit, split)
 };
 AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t max_q, int64_t max_len, int64_t window);
 hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
+// kv_attention_tile.hip
+hipError_t launch_kv_attention_tile(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
+constexpr int attn_tile_max(int dim) { return dim == 64 ? 4 : dim == 128 ? 3 : 2; }
+// (split, row) pairs that the join of a split unit holds in LDS.
+constexpr int kStreamJoin = 4096, kTileJoin = 8192;
 
 }  // namespace nvfp4
