@@ -81,8 +81,8 @@ AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t max_q, in
 hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
 // kv_attention_tile.hip
 hipError_t launch_kv_attention_tile(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
-constexpr int attn_tile_max(int dim) { return dim == 64 ? 4 : dim == 128 ? 3 : 2; }
-// (split, row) pairs that the join of a split unit holds in LDS.
-constexpr int kStreamJoin = 4096, kTileJoin = 8192;
+constexpr int attn_tile_max(int dim) { return dim == 64 ? 4 : 2; }  // most row tiles of a wave
+// (split, row) pairs that kv_attention.hip's join of a split unit holds in LDS.
+constexpr int kStreamJoin = 4096;
 
 }  // namespace nvfp4

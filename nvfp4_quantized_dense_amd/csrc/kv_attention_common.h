@@ -17,6 +17,8 @@
 // record's V codes are stored in the same token order, so the probabilities
 // never leave their registers, and the row statistics are one number a lane.
 #pragma once
+#include <type_traits>
+
 #include "attention.h"
 #include "kv_layout.h"
 
@@ -47,6 +49,15 @@ __device__ __forceinline__ f16x4 e4m3x4_f16(uint32_t w) {
   return f16x4{a[0], a[1], b[0], b[1]};
 }
 
+// f(0), .., f(N - 1) with the number as a constant.
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for<N, I + 1>(f);
+  }
+}
+
 // ---- operands from a record ----------------------------------------------
 
 // A lane's share of a record's K: the codes and scales of its token.
@@ -54,16 +65,19 @@ template <int D>
 struct KFrag {
   uint32_t c[D / 32], s;
 };
-// Of V: the codes of its channel, and the scales of block lane % (D / 16) of
-// its quad (the other blocks' are with the quad's other lanes).
-template <int D>
+// Of V: the codes of its channel in all blocks or, PARTS = 2, in one half of
+// them, and the scales of one of these blocks, lane % (D / 16 / PARTS), of its
+// quad (the other blocks' are with the quad's other lanes).
+template <int D, int PARTS = 1>
 struct VFrag {
-  uint32_t c[D / 32], s;
+  uint32_t c[D / 32 / PARTS], s;
 };
 
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t* p) {
-  if constexpr (N == 2) {
+  if constexpr (N == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
     const u32x2 t = *reinterpret_cast<const u32x2*>(p);
     w[0] = t[0]; w[1] = t[1];
   } else {
@@ -76,17 +90,18 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t* p) {
 }
 
 template <int D>
-__device__ __forceinline__ void load_k(KFrag<D>& f, const uint8_t* rec, int lane) {
+__device__ __forceinline__ void load_k(KFrag<D>& f, const uint8_t* rec, unsigned lane) {
   load_words(f.c, rec + lane * KvRec<D>::kLane);
   const uint8_t* s = rec + KvRec<D>::kKs + lane * (D / 64);
   if constexpr (D == 64) f.s = *s;
   else if constexpr (D == 128) f.s = *reinterpret_cast<const uint16_t*>(s);
   else f.s = *reinterpret_cast<const uint32_t*>(s);
 }
-template <int D>
-__device__ __forceinline__ void load_v(VFrag<D>& f, const uint8_t* rec, int lane) {
-  load_words(f.c, rec + KvRec<D>::kV + lane * KvRec<D>::kLane);
-  f.s = *reinterpret_cast<const uint32_t*>(rec + KvRec<D>::kVs + (lane >> 4) * (D / 4) + (lane & (D / 16 - 1)) * 4);
+template <int D, int PARTS>
+__device__ __forceinline__ void load_v(VFrag<D, PARTS>& f, const uint8_t* rec, unsigned lane, unsigned part) {
+  constexpr int kN = D / 16 / PARTS;
+  load_words(f.c, rec + KvRec<D>::kV + lane * KvRec<D>::kLane + part * (2 * kN));
+  f.s = *reinterpret_cast<const uint32_t*>(rec + KvRec<D>::kVs + (lane >> 4) * (D / 4) + (part * kN + (lane & (kN - 1))) * 4);
 }
 
 // Lane N's value in each row of 16 lanes.
@@ -95,9 +110,10 @@ __device__ __forceinline__ uint32_t row_bcast(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x150 + N, 0xF, 0xF, true);
 }
 
-// V^T of channel block Y as an operand: 4 tokens of each of two records.
-template <int D, int Y>
-__device__ __forceinline__ f16x8 v_operand(const VFrag<D> (&f)[2], const f16x4 (&vs)[2]) {
+// V^T of channel block Y (of f's) as an operand: 4 tokens of each of two
+// records.
+template <int Y, int D, int PARTS>
+__device__ __forceinline__ f16x8 v_operand(const VFrag<D, PARTS> (&f)[2], const f16x4 (&vs)[2]) {
   f16x8 r;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
@@ -109,6 +125,51 @@ __device__ __forceinline__ f16x8 v_operand(const VFrag<D> (&f)[2], const f16x4 (
   }
   return r;
 }
+
+// The records of head h in the pages of a block table row, one after the
+// other: where record (page slot ps, group `in`) is. 64 page numbers, of the
+// slots from tab0 on, are in the lanes of `tab`; slots past `last` stand for
+// that one (its keys are masked). A page number outside the cache makes `ok`
+// false and the address that of page 0.
+template <int D>
+struct Walk {
+  const int32_t* table;
+  const uint8_t* base;
+  uint64_t page_bytes;
+  unsigned pages;
+  int groups, last, ps, in, tab0, tab;
+  __device__ __forceinline__ void load_tab(int lane) {
+    const int at = tab0 + lane;
+    tab = table[at < last ? at : last];
+    asm volatile("" : "+v"(tab));  // waits here, not at each use for all loads in flight
+  }
+  // From group g on, the last key's group being g_last.
+  __device__ __forceinline__ Walk(const AttnArgs& a, unsigned b, int h, int g, int g_last, int lane) {
+    groups = a.c.page_size / 16;
+    table = a.table + (int64_t)b * a.table_stride;
+    base = a.c.cache + (uint64_t)h * groups * KvRec<D>::kBytes;
+    page_bytes = (uint64_t)a.c.heads * groups * KvRec<D>::kBytes;
+    pages = (unsigned)a.c.pages;
+    last = g_last / groups;
+    ps = g / groups;
+    in = g - ps * groups;
+    tab0 = ps;
+    load_tab(lane);
+  }
+  __device__ __forceinline__ const uint8_t* record(bool& ok, int lane) {
+    if (ps - tab0 >= 64) {
+      tab0 = ps;
+      load_tab(lane);
+    }
+    const unsigned page = (unsigned)__builtin_amdgcn_readlane(tab, ps - tab0);
+    ok = page < pages;
+    return base + (ok ? page : 0u) * page_bytes + (unsigned)in * KvRec<D>::kBytes;
+  }
+  __device__ __forceinline__ void step(int by) {
+    in += by;
+    while (in >= groups) { in -= groups; ++ps; }
+  }
+};
 
 // Keeps the bytes of the quad's tokens first .. first + 3 that lie in [lo, hi).
 __device__ __forceinline__ uint32_t byte_mask(int first, int lo, int hi) {
@@ -154,6 +215,21 @@ __device__ __forceinline__ int sees_hi(const Seq& s, int i) {
 }
 __device__ __forceinline__ int sees_lo(int hi, int64_t window) {
   return window > 0 && hi > window ? (int)(hi - window) : 0;
+}
+
+// The keys [lo, hi) that any of a workgroup's rows sees (rows row0 on, row0
+// one of them), walked over from `start` on in `splits` stretches.
+struct Stretch {
+  int lo, hi, start, splits;
+};
+__device__ __forceinline__ Stretch active_splits(const AttnArgs& a, const AttnPlan& p, const Seq& seq, int row0, int rows, int G) {
+  const int last = seq.rows - 1 < row0 + rows - 1 ? seq.rows - 1 : row0 + rows - 1;
+  Stretch s;
+  s.hi = sees_hi(seq, last / G);
+  s.lo = sees_lo(sees_hi(seq, row0 / G), a.window);
+  s.start = s.lo & ~31;
+  s.splits = s.hi > s.lo ? (s.hi - s.start + p.chunk - 1) / p.chunk : 1;
+  return s;
 }
 
 // RT tiles of 16 rows: lane (quad, col) holds row col of a tile, of its output
@@ -246,21 +322,25 @@ __device__ __forceinline__ void hide_scores(const Rows<D, RT>& r, f32x4 (&sc)[RT
   }
 }
 
-// Probabilities of a pair's scores, as operands. The subtracted maximum
-// follows the true one only when a score passes it by more than 2^8 in
-// probability: f16 holds probabilities up to that as exactly as up to 1, and
-// most steps then need neither the exchange between lanes nor the rescaling.
-template <int D, int RT>
-__device__ __forceinline__ void softmax_pair(Rows<D, RT>& r, const f32x4 (&sc)[RT][2], f16x8 (&pf)[RT]) {
-  float mx[RT];
-  bool passed = false;
+template <int RT>
+__device__ __forceinline__ void lane_maximum(const f32x4 (&sc)[RT][2], float (&mx)[RT]) {
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     mx[t] = sc[t][0][0];
 #pragma unroll
     for (int e = 1; e < 8; ++e) mx[t] = __builtin_fmaxf(mx[t], sc[t][e >> 2][e & 3]);
-    passed |= mx[t] > r.t[t];
   }
+}
+
+// mx: the maximum of a pair's scores in this lane. The subtracted maximum
+// follows the true one only when a score passes it by more than 2^8 in
+// probability: f16 holds probabilities up to that as exactly as up to 1, and
+// most steps then need neither the exchange between lanes nor the rescaling.
+template <int D, int RT>
+__device__ __forceinline__ void renew_maximum(Rows<D, RT>& r, const float (&mx)[RT]) {
+  bool passed = false;
+#pragma unroll
+  for (int t = 0; t < RT; ++t) passed |= mx[t] > r.t[t];
   if (__any(passed)) {
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
@@ -274,6 +354,11 @@ __device__ __forceinline__ void softmax_pair(Rows<D, RT>& r, const f32x4 (&sc)[R
       for (int y = 0; y < D / 16; ++y) r.o[t][y] *= alpha;
     }
   }
+}
+
+// Probabilities of a pair's scores, as operands.
+template <int D, int RT>
+__device__ __forceinline__ void probabilities(Rows<D, RT>& r, const f32x4 (&sc)[RT][2], f16x8 (&pf)[RT]) {
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     const float mf = -r.m[t] * r.f[t];
@@ -317,64 +402,6 @@ __device__ __forceinline__ void store4(const AttnArgs& a, int64_t at, const f32x
 __device__ __forceinline__ int64_t out_row(const AttnArgs& a, const Seq& seq, int row, int h, int G) {
   const int i = (int)((unsigned)row / (unsigned)G);
   return (seq.q0 + i) * a.heads_q + h * G + (row - i * G);
-}
-
-// Partials of a split: [kRows] m, [kRows] l, [kRows][D] o. Each wave's are at
-// device scope before its workgroup counts as arrived; true for the last one
-// of `active`, which resets the count for the next launch.
-__device__ __forceinline__ bool split_last(uint32_t* counter, int active, uint32_t* arrived) {
-  __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  __builtin_amdgcn_s_waitcnt(0x3F70);  // vmcnt(0)
-  __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  __syncthreads();
-  if (threadIdx.x == 0) *arrived = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  if (*arrived != (uint32_t)(active - 1)) return false;
-  if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  return true;
-}
-
-// Joins the splits of a unit in split order, so that the result does not
-// depend on which workgroup arrived last. lds: 2 kJoin floats.
-template <int D, int kRows, int kJoin>
-__device__ __forceinline__ void join_splits(const AttnArgs& a, const AttnPlan& p, const Seq& seq, unsigned unit, int active,
-                                            int row0, int h, int G, float* lds) {
-  const float vg = *a.v_g;
-  const float* parts = a.part + (int64_t)unit * p.splits * p.part_floats;
-  const Rsrc ra = make_rsrc(parts, (uint32_t)(active * p.part_floats * 4));
-  float* jm = lds;  // [active][kRows] m, then l
-  float* jl = lds + kJoin;
-  for (int n = threadIdx.x; n < active * kRows; n += blockDim.x) {
-    const uint32_t at = (uint32_t)((n / kRows * p.part_floats + n % kRows) * 4);
-    jm[n] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(ra, (int)at, 0, 16));
-    jl[n] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(ra, (int)at, 4 * kRows, 16));
-  }
-  __syncthreads();
-  const int live = seq.rows - row0 < kRows ? seq.rows - row0 : kRows;
-  for (int n = threadIdx.x; n < live * (D / 4); n += blockDim.x) {
-    const int rr = n / (D / 4), d = n % (D / 4) * 4;
-    float m = kNoKey;
-    for (int s = 0; s < active; ++s) m = __builtin_fmaxf(m, jm[s * kRows + rr]);
-    float l = 0.0f;
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    const uint32_t at = (uint32_t)(8 * kRows + (rr * D + d) * 4);
-    for (int s = 0; s < active; s += 8) {
-      f32x4 x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e)  // past the last split: zeros, unread
-        x[e] = __builtin_bit_cast(f32x4, bload16_dev(ra, s + e < active ? at + (uint32_t)((s + e) * p.part_floats * 4) : kOutOfRange));
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (s + e >= active) break;
-        const float w = __builtin_amdgcn_exp2f(jm[(s + e) * kRows + rr] - m);
-        l += w * jl[(s + e) * kRows + rr];
-        v += x[e] * w;
-      }
-    }
-    const int64_t orow = out_row(a, seq, row0 + rr, h, G);
-    store4(a, orow * D + d, v * inverse_sum(l, vg));
-    if (d == 0 && a.lse != nullptr) a.lse[orow] = lse_of(m, l);
-  }
 }
 
 #endif  // __HIP_DEVICE_COMPILE__

@@ -6,8 +6,15 @@
 // head's group), 16 RT a wave, and walks over its keys in tiles of 64. A
 // tile's codes are made f16 once for all four waves, a quarter by each, and
 // lie in LDS in the order in which the matrix instruction's lanes read them,
-// so that neither side has a bank conflict. Two tiles are in LDS, a third is
-// on its way in registers, one barrier per tile.
+// so that neither side has a bank conflict.
+//
+// What bounds it is the waves' instruction issue: per 32 keys and 32 rows (D
+// 128) 32 matrix instructions stand against 70 of the softmax and 50 of
+// making f16 and fetching. So the three overlap: while the probabilities of
+// 32 keys are computed, the scores of the next 32 are on the matrix core, and
+// while values are added, the tile after the next is made. RT 2 at D 128 (4
+// at 64): 16 rows a wave more would spill, fewer share the making less (8 x
+// 1536 tokens x 64 heads over 8192 keys: RT 1 / 2 4215 / 2920 us).
 #include "kv_attention_common.h"
 
 namespace nvfp4 {
@@ -16,24 +23,19 @@ namespace {
 #if defined(__HIP_DEVICE_COMPILE__)
 constexpr int kTile = 64;  // keys
 
-// Writes V's operands of a pair, channel blocks Y on, `to` being the first's.
-template <int D, int Y>
-__device__ __forceinline__ void put_v(f16x8* to, const VFrag<D> (&f)[2], const f16x4 (&vs)[2]) {
-  to[Y * 64] = v_operand<D, Y>(f, vs);
-  if (Y & 1) __builtin_amdgcn_sched_barrier(0);  // few operands in flight: registers
-  if constexpr (Y + 1 < D / 16) put_v<D, Y + 1>(to, f, vs);
-}
 #endif
 
 template <int D, int RT>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(AttnArgs a, AttnPlan p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int kB = D / 16, kW = D / 32, kRows = 64 * RT;
-  constexpr int kOps = 4 * kW + 2 * kB;  // operands of a tile: [4 records][kW] K, [2 pairs][kB] V
-  constexpr int kJoin = kTileJoin, kAhead = 4;
-  __shared__ f16x8 lds[2 * kOps * 64 * 2 > kJoin ? 2 * kOps * 64 : kJoin / 2];
-  __shared__ uint32_t page_ok[2][2];  // of a tile's pairs: bit x for record x
-  __shared__ uint32_t arrived;
+  // Operands: [2 tiles][4 records][kW] K, [2 tiles][kB] V of the first pair,
+  // [3 tiles][kB] V of the second, which is read while the barrier that
+  // parts two tiles is already behind (one barrier a tile, not two).
+  constexpr int kV = 8 * kW, kV2 = kV + 2 * kB, kOps = kV2 + 3 * kB;
+  constexpr int kAhead = 4;
+  __shared__ f16x8 lds[kOps * 64];
+  __shared__ alignas(4) uint8_t page_ok[2][4];  // of a tile's records
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
   const int G = a.heads_q / a.c.heads;
@@ -47,12 +49,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
   const Seq seq = seq_of(a, b, G);
   if ((int64_t)rb * kRows >= seq.rows) return;
   const int row0 = (int)rb * kRows;
-  const int last_row = seq.rows - 1 < row0 + kRows - 1 ? seq.rows - 1 : row0 + kRows - 1;
-  const int hi_all = sees_hi(seq, last_row / G), lo_all = sees_lo(sees_hi(seq, row0 / G), a.window);
-  const int start = lo_all & ~31;
-  const int active = hi_all > lo_all ? (hi_all - start + p.chunk - 1) / p.chunk : 1;
+  const Stretch all = active_splits(a, p, seq, row0, kRows, G);
+  const int hi_all = all.hi, lo_all = all.lo, active = all.splits;
   if (split >= active) return;
-  const int s_first = start + split * p.chunk;
+  const int s_first = all.start + split * p.chunk;
   const int s_last = hi_all - s_first > p.chunk ? s_first + p.chunk : hi_all;
   const int tiles = s_last > s_first ? (s_last - s_first + kTile - 1) / kTile : 0;
 
@@ -66,168 +66,219 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
     lo_full = sees_lo(sees_hi(seq, (seq.rows < wrow0 + 16 * RT ? seq.rows - 1 : wrow0 + 16 * RT - 1) / G), a.window);
   }
 
-  // Waves 0 and 1 bring K of the tile's first and second pair of records,
-  // waves 2 and 3 V. The pair's first group is group `in` of page slot `ps`,
-  // whose page number is in a lane of `tab` (64 slots from tab0 on); slots
-  // past the last key's stand for that one and are masked.
-  const int groups = a.c.page_size / 16, pair = wave & 1;
-  const bool is_v = wave >= 2;
-  const int32_t* table = a.table + (int64_t)b * a.table_stride;
-  const int g0 = (s_first >> 4) + 2 * pair;
-  int ps = g0 / groups, in = g0 - ps * groups, tab0 = ps, tab = 0;
-  const int ps_last = hi_all > 0 ? ((hi_all - 1) >> 4) / groups : 0;
-  auto load_tab = [&] {
-    const int at = tab0 + lane;
-    tab = table[at < ps_last ? at : ps_last];
-  };
-  KFrag<D> f[2];  // K's or V's codes and scales: one shape
-  uint32_t ok = 0;
-  auto step = [&](int by) {
-    in += by;
-    while (in >= groups) { in -= groups; ++ps; }
-  };
-  auto fetch = [&] {
-    ok = 0;
+  // Wave w brings K of the tile's record w and half w & 1 of V's channels of
+  // the pair w >> 1.
+  const int pair = wave >> 1, half = wave & 1;
+  KFrag<D> fk;
+  VFrag<D, 2> fv[2];
+  bool ok[2] = {true, true};
+  // Before what was fetched becomes operands: tokens no row sees may never
+  // have been written. Their V scales become zero, so that no NaN code meets
+  // a zero probability. `base`: the tile's first key.
+  auto clear_v = [&](int base) {
+    base += 32 * pair;
+    if (base < lo_all || base + 32 > hi_all || !ok[0] || !ok[1]) {
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      if (ps - tab0 >= 64) {
-        tab0 = ps;
-        load_tab();
-      }
-      const int page = __builtin_amdgcn_readlane(tab, ps - tab0);
-      const bool good = page >= 0 && page < a.c.pages;
-      ok |= good ? 1u << x : 0u;
-      const uint8_t* rec = a.c.cache + rec_offset<D>(good ? page : 0, a.c.heads, h, groups, in);
-      if (is_v) load_v<D>(reinterpret_cast<VFrag<D>&>(f[x]), rec, lane);
-      else load_k<D>(f[x], rec, lane);
-      step(x == 0 ? 1 : 3);
+      for (int x = 0; x < 2; ++x) fv[x].s &= ok[x] ? byte_mask(base + 16 * x + 4 * quad, lo_all, hi_all) : 0u;
     }
   };
-  // The fetched pair becomes operands of buffer `buf`; its first key is `base`.
-  auto put = [&](int buf, int base) {
-    f16x8* to = lds + buf * kOps * 64 + lane;
-    if (is_v) {
-      VFrag<D> v[2];
+  // Operand n of the kB that this wave makes of what it fetched: K and V in
+  // turn, for buffers `buf` and `third`.
+  f16x4 ks, vs[2];
+  auto scales = [&] {
+    ks = e4m3x4_f16(fk.s);
+    vs[0] = e4m3x4_f16(fv[0].s);
+    vs[1] = e4m3x4_f16(fv[1].s);
+  };
+  auto put = [&](auto n, int buf, int third) {
+    constexpr int kN = decltype(n)::value, kS = kN / 2;
+    if constexpr (kN % 2 == 0) lds[((4 * buf + wave) * kW + kS) * 64 + lane] = deq8_f16(fk.c[kS], ks[kS >> 1]);
+    else lds[((pair == 0 ? kV + buf * kB : kV2 + third * kB) + half * (kB / 2) + kS) * 64 + lane] = v_operand<kS>(fv, vs);
+  };
+  // One pair: its probabilities from the scores `now` while the matrix core
+  // computes the next pair's scores `later`, K from operand k0 on; then its
+  // values, V from operand v0 on, while make(0 .. kB - 1) fills in. Operands
+  // are read kAhead products before they are used. The barriers keep this
+  // order, and few registers alive.
+  auto attend = [&](const f32x4 (&now)[RT][2], f32x4 (&later)[RT][2], float (&mx)[RT], int k0, int v0, auto&& make) {
+    const f16x8 *kp = lds + k0 * 64 + lane, *vp = lds + v0 * 64 + lane;
+    f16x8 op[kAhead], pf[RT];
+    auto operand = [&](int n) { return n < 2 * kW ? kp[n * 64] : vp[(n - 2 * kW) * 64]; };
+    float mf[RT], e[RT];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        v[x] = reinterpret_cast<VFrag<D>&>(f[x]);
-        // Tokens no row sees may never have been written: their V scales
-        // become zero, so that no NaN code meets a zero probability.
-        if (base < lo_all || base + 32 > hi_all || ok != 3u)
-          v[x].s &= (ok >> x) & 1 ? byte_mask(base + 16 * x + 4 * quad, lo_all, hi_all) : 0u;
-      }
-      const f16x4 vs[2] = {e4m3x4_f16(v[0].s), e4m3x4_f16(v[1].s)};
-      put_v<D, 0>(to + (4 * kW + pair * kB) * 64, v, vs);
-    } else {
+    for (int t = 0; t < RT; ++t) {
+      mf[t] = -r.m[t] * r.f[t];
+      later[t][0] = later[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const f16x4 ks = e4m3x4_f16(f[x].s);
+    for (int n = 0; n < kAhead; ++n) op[n] = operand(n);
+    static_for<2 * kW>([&](auto step) {
+      constexpr int n = decltype(step)::value;
 #pragma unroll
-        for (int s = 0; s < kW; ++s) {
-          to[((2 * pair + x) * kW + s) * 64] = deq8_f16(f[x].c[s], ks[s >> 1]);
-          if (s & 1) __builtin_amdgcn_sched_barrier(0);
+      for (int t = 0; t < RT; ++t) {
+        later[t][n / kW] = mfma16x16x32(op[n % kAhead], r.q[t][n % kW], later[t][n / kW]);
+#pragma unroll
+        for (int i = 8 * n / (2 * kW); i < 8 * (n + 1) / (2 * kW); ++i) {
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(now[t][i >> 2][i & 3], r.f[t], mf[t]));
+          r.l[t] += p;
+          if (i & 1) { pf[t][i - 1] = (_Float16)e[t]; pf[t][i] = (_Float16)p; }
+          e[t] = p;
         }
       }
-      if (lane == 0) page_ok[buf][pair] = ok;
-    }
-  };
-  auto attend = [&](int buf, int base) {
-    const f16x8* from = lds + buf * kOps * 64 + lane;
-#pragma unroll 1
-    for (int pr = 0; pr < 2; ++pr) {
-      const int at = base + 32 * pr;
-      const uint32_t has = __builtin_amdgcn_readfirstlane(page_ok[buf][pr]);
-      const bool edge = at + 32 > hi_full || at < lo_full || has != 3u;
-      f32x4 sc[RT][2];
-#pragma unroll
-      for (int t = 0; t < RT; ++t) sc[t][0] = sc[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-      // Operands are read kAhead products before they are used.
-      const f16x8* kp = from + 2 * pr * kW * 64;
-      f16x8 op[kAhead];
-#pragma unroll
-      for (int n = 0; n < kAhead; ++n) op[n] = kp[n * 64];
-#pragma unroll
-      for (int n = 0; n < 2 * kW; ++n) {
-#pragma unroll
-        for (int t = 0; t < RT; ++t) sc[t][n / kW] = mfma16x16x32(op[n % kAhead], r.q[t][n % kW], sc[t][n / kW]);
-        if (n + kAhead < 2 * kW) op[n % kAhead] = kp[(n + kAhead) * 64];
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if (edge) {
-        asm volatile("");  // a branch: most tiles need no mask
-        const bool okx[2] = {(has & 1) != 0, (has & 2) != 0};
-        hide_scores<D, RT>(r, sc, at, quad, okx);
-      }
-      f16x8 pf[RT];
-      softmax_pair<D, RT>(r, sc, pf);
-      const f16x8* vp = from + (4 * kW + pr * kB) * 64;
-#pragma unroll
-      for (int n = 0; n < kAhead; ++n) op[n] = vp[n * 64];
+      op[n % kAhead] = operand(n + kAhead);
       __builtin_amdgcn_sched_barrier(0);
+    });
+    static_for<kB>([&](auto step) {
+      constexpr int y = decltype(step)::value, n = 2 * kW + y;
 #pragma unroll
-      for (int y = 0; y < kB; ++y) {
+      for (int t = 0; t < RT; ++t) r.o[t][y] = mfma16x16x32(op[n % kAhead], pf[t], r.o[t][y]);
+      if constexpr (y + kAhead < kB) op[n % kAhead] = operand(n + kAhead);
+      make(step);
+      // The next pair's maximum, by lane.
 #pragma unroll
-        for (int t = 0; t < RT; ++t) r.o[t][y] = mfma16x16x32(op[y % kAhead], pf[t], r.o[t][y]);
-        if (y + kAhead < kB) op[y % kAhead] = vp[(y + kAhead) * 64];
-        __builtin_amdgcn_sched_barrier(0);
+      for (int i = 8 * y / kB; i < 8 * (y + 1) / kB; ++i) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+          mx[t] = i == 0 ? later[t][0][0] : __builtin_fmaxf(mx[t], later[t][i >> 2][i & 3]);
       }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+#pragma unroll
+    for (int t = 0; t < RT; ++t) asm volatile("" : "+v"(mx[t]), "+v"(r.l[t]));  // computed in here
+  };
+  auto renew = [&](f32x4 (&sc)[RT][2], float (&mx)[RT], int at, uint32_t oks) {
+    if (at + 32 > hi_full || at < lo_full || oks != 0x101u) {
+      asm volatile("");  // a branch: most pairs need no mask
+      const bool okx[2] = {(oks & 255u) != 0, oks >> 8 != 0};
+      hide_scores<D, RT>(r, sc, at, quad, okx);
+      lane_maximum<RT>(sc, mx);
     }
+    renew_maximum<D, RT>(r, mx);
+  };
+  auto make_tile = [&](int buf, int third) {
+    scales();
+    static_for<kB>([&](auto n) { put(n, buf, third); });
+    if (lane == 0) page_ok[buf][wave] = ok[half];
   };
   if (tiles > 0) {
-    load_tab();
+    Walk<D> walk(a, b, h, (s_first >> 4) + 2 * pair, (hi_all - 1) >> 4, lane);
+    auto fetch = [&] {
+      const uint8_t* rec[2];
+      rec[0] = walk.record(ok[0], lane);
+      walk.step(1);
+      rec[1] = walk.record(ok[1], lane);
+      walk.step(3);
+      load_v(fv[0], rec[0], lane, half);
+      load_v(fv[1], rec[1], lane, half);
+      load_k(fk, half ? rec[1] : rec[0], lane);
+    };
     fetch();
-    put(0, s_first + 32 * pair);
-    if (tiles > 1) fetch();
+    clear_v(s_first);
+    make_tile(0, 0);
+    fetch();
+    clear_v(s_first + kTile);
+    make_tile(1, 1);
+    fetch();
     __syncthreads();
-    for (int j = 0; j < tiles; ++j) {
-      const int base = s_first + kTile * j;
-      if (j + 1 < tiles) {
-        put((j + 1) & 1, base + kTile + 32 * pair);
-        if (j + 2 < tiles) fetch();
-      }
-      attend(j & 1, base);
+    f32x4 sa[RT][2], sb[RT][2];
+    float mx[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) sa[t][0] = sa[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < 2 * kW; ++n) {
+      const f16x8 op = lds[n * 64 + lane];
+#pragma unroll
+      for (int t = 0; t < RT; ++t) sa[t][n / kW] = mfma16x16x32(op, r.q[t][n % kW], sa[t][n / kW]);
+    }
+    lane_maximum<RT>(sa, mx);
+    uint32_t oks = __builtin_amdgcn_readfirstlane(*reinterpret_cast<const uint32_t*>(page_ok[0]));
+    // Tile j's first pair, then its second while tile j + 2 is made of what a
+    // whole tile's time ago was asked for. After the barrier tile j + 1 is
+    // there and K and the first pair's V of tile j have been read by all.
+    for (int j = 0, third = 0; j < tiles; ++j) {
+      const int base = s_first + kTile * j, buf = j & 1, third2 = third == 0 ? 2 : third - 1;
+      renew(sa, mx, base, oks & 0xFFFFu);
+      attend(sa, sb, mx, (4 * buf + 2) * kW, kV + buf * kB, [](auto) {});
+      renew(sb, mx, base + 32, oks >> 16);
+      clear_v(base + 2 * kTile);
       __syncthreads();
+      const uint32_t flags = *reinterpret_cast<const uint32_t*>(page_ok[buf ^ 1]);
+      scales();
+      attend(sb, sa, mx, 4 * (buf ^ 1) * kW, kV2 + third * kB, [&](auto n) { put(n, buf, third2); });
+      if (lane == 0) page_ok[buf][wave] = ok[half];
+      oks = __builtin_amdgcn_readfirstlane(flags);
+      fetch();
+      third = third == 2 ? 0 : third + 1;
     }
   }
   finish_rows<D, RT>(r);
 
   const float vg = *a.v_g;
+  // Partials of a split: [kRows] m, [kRows] l, [kRows][D] o.
   float* part = a.part + ((int64_t)unit * p.splits + split) * p.part_floats;
-  const Rsrc rp = make_rsrc(part, (uint32_t)(p.part_floats * 4));
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     const int rr = wave * 16 * RT + 16 * t + col;
-    const bool live = row0 + rr < seq.rows;
+    if (row0 + rr >= seq.rows) continue;
     if (active == 1) {
-      if (!live) continue;
       const float inv = inverse_sum(r.l[t], vg);
       const int64_t orow = out_row(a, seq, row0 + rr, h, G);
 #pragma unroll
       for (int y = 0; y < kB; ++y) store4(a, orow * D + 16 * y + 4 * quad, r.o[t][y] * inv);
       if (quad == 0 && a.lse != nullptr) a.lse[orow] = lse_of(r.m[t], r.l[t]);
     } else {
-      if (live) {
 #pragma unroll
-        for (int y = 0; y < kB; ++y)
-          bstore16_dev(rp, (uint32_t)(8 * kRows + (rr * D + 16 * y + 4 * quad) * 4), __builtin_bit_cast(u32x4, r.o[t][y]));
-      }
+      for (int y = 0; y < kB; ++y)
+        *reinterpret_cast<f32x4*>(part + 2 * kRows + rr * D + 16 * y + 4 * quad) = r.o[t][y];
       if (quad == 0) {
-        __hip_atomic_store(part + rr, r.m[t], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __hip_atomic_store(part + kRows + rr, r.l[t], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        part[rr] = r.m[t];
+        part[kRows + rr] = r.l[t];
       }
     }
   }
-  if (active == 1) return;
-  if (!split_last(a.counters + unit, active, &arrived)) return;
-  join_splits<D, kRows, kJoin>(a, p, seq, unit, active, row0, h, G, reinterpret_cast<float*>(lds));
 #endif  // __HIP_DEVICE_COMPILE__
+}
+
+// The join of split units, in split order: 1024 / D rows a workgroup, four
+// channels a thread. In one workgroup a unit (the last to arrive) it took 5 us
+// a split; spread over the chip it takes about 5 us in all.
+template <int D>
+__global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, AttnPlan p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const int rows_wg = 64 * p.row_tiles, G = a.heads_q / a.c.heads;
+  const unsigned unit = blockIdx.x, heads = a.c.heads, blocks = p.row_blocks;
+  const int h = (int)(unit % heads);
+  const unsigned rb = blocks - 1 - unit / heads % blocks, b = unit / heads / blocks;
+  const Seq seq = seq_of(a, b, G);
+  const int rr = blockIdx.y * (1024 / D) + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
+  if ((int64_t)rb * rows_wg + rr >= seq.rows) return;
+  const int row0 = (int)rb * rows_wg;
+  const int active = active_splits(a, p, seq, row0, rows_wg, G).splits;
+  if (active == 1) return;
+  const float* part = a.part + (int64_t)unit * p.splits * p.part_floats;
+  float m = kNoKey;
+  for (int s = 0; s < active; ++s) m = __builtin_fmaxf(m, part[(int64_t)s * p.part_floats + rr]);
+  float l = 0.0f;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < active; ++s) {
+    const float* ps = part + (int64_t)s * p.part_floats;
+    const float w = __builtin_amdgcn_exp2f(ps[rr] - m);
+    l += w * ps[rows_wg + rr];
+    v += *reinterpret_cast<const f32x4*>(ps + 2 * rows_wg + rr * D + d) * w;
+  }
+  const int64_t orow = out_row(a, seq, row0 + rr, h, G);
+  store4(a, orow * D + d, v * inverse_sum(l, *a.v_g));
+  if (d == 0 && a.lse != nullptr) a.lse[orow] = lse_of(m, l);
+#endif
 }
 
 template <int D, int RT>
 void launch_rt(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
   if constexpr (RT <= attn_tile_max(D)) {
-    if (p.row_tiles == RT) k_kv_attention_tile<D, RT><<<dim3((unsigned)p.units, (unsigned)p.splits), dim3(256), 0, s>>>(a, p);
-    else launch_rt<D, RT + 1>(a, p, s);
+    if (p.row_tiles != RT) return launch_rt<D, RT + 1>(a, p, s);
+    k_kv_attention_tile<D, RT><<<dim3((unsigned)p.units, (unsigned)p.splits), dim3(256), 0, s>>>(a, p);
+    if (p.splits > 1) k_kv_join<D><<<dim3((unsigned)p.units, (unsigned)(64 * RT * D / 1024)), dim3(256), 0, s>>>(a, p);
   }
 }
 
