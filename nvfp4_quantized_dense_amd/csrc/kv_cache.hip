@@ -25,20 +25,6 @@ __device__ __forceinline__ Slot slot_at(int64_t slot, int64_t pages, int page_si
   return r;
 }
 
-// A V code byte holds two tokens and an aligned quad of tokens shares 16-bit
-// units, so list entries t - a .. t - a + 3 that fill an aligned quad are
-// handled together by the first of them. -1: entry t belongs to the quad of
-// an earlier entry, 4: it leads a quad, 1: it stands alone.
-__device__ __forceinline__ int quad_role(const int64_t* slots, int64_t T, int64_t t, int64_t slot) {
-  const int a = (int)(slot & 3);
-  const int64_t first = t - a;
-  if (first < 0 || first + 3 >= T) return 1;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (slots[first + i] != slot - a + i) return 1;
-  return a == 0 ? 4 : -1;
-}
-
 template <bool F32>
 __device__ __forceinline__ void load8_at(const void* base, int64_t elem, float (&v)[8]) {
   if constexpr (F32) {
@@ -85,139 +71,222 @@ __device__ __forceinline__ uint32_t quant8(const float (&v)[8], float g_inv, uin
   return e2m1_pack8(y);
 }
 
-// One thread per (list entry, head, 8 channels).
+// A wave takes four list entries, a row of 16 lanes each, and 16 units of the
+// entry's heads x D / 8. Of K a unit is 8 channels. Of V it is channels
+// 4 c4 + [0, 4) of blocks 2 m and 2 m + 1: what the record stores of them for
+// a quad of tokens is then a dword per channel.
+template <int D>
+struct Unit {
+  int h, j, m, c4;
+  bool ok;
+};
+template <int D>
+__device__ __forceinline__ Unit<D> unit_at(unsigned u, int heads) {
+  Unit<D> r;
+  r.h = (int)(u / (D / 8));
+  r.j = (int)(u % (D / 8));
+  r.m = r.j >> 2;
+  r.c4 = r.j & 3;
+  r.ok = r.h < heads;
+  return r;
+}
+// Where unit u's V dwords of a quad begin, and its scale bytes.
+template <int D>
+__device__ __forceinline__ int v_at(const Unit<D>& u, int q) {
+  return KvRec<D>::kV + (q * 16 + 4 * u.c4) * KvRec<D>::kLane + 4 * u.m;
+}
+template <int D>
+__device__ __forceinline__ int vs_at(const Unit<D>& u, int q) {
+  return KvRec<D>::kVs + (q * (D / 16) + 2 * u.m) * 4;
+}
+
+template <bool F32>
+__device__ __forceinline__ void load4_at(const void* base, int64_t elem, float* v) {
+  if constexpr (F32) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(base) + elem);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = a[i];
+  } else {
+    const u32x2 a = *reinterpret_cast<const u32x2*>(reinterpret_cast<const uint16_t*>(base) + elem);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v[2 * i] = __uint_as_float(a[i] << 16);
+      v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+// Two of V's blocks, 4 channels of each in this lane and the others in the
+// neighbours': 8 codes (block 2 m in the low half) and the scale bytes.
+__device__ __forceinline__ uint32_t quant44(const float (&v)[8], float g_inv, uint32_t (&scale)[2]) {
+  float y[8];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(v[4 * x + i]) & 0x7FFFFFFFu);
+    m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 2));
+    const BlockScale bs = block_scale(__uint_as_float(m), g_inv);
+    scale[x] = bs.byte;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[4 * x + i] = v[4 * x + i] * bs.r;
+  }
+  return e2m1_pack8(y);
+}
+
+// Row k of four holds the codes of token k of a quad, a nibble a channel;
+// becomes the codes of channel k, a nibble a token (both halves alike).
+__device__ __forceinline__ uint32_t quad_transpose(uint32_t w, int k) {
+  const uint32_t p = (uint32_t)__shfl_xor((int)w, 16);
+  w = k & 1 ? ((p >> 4) & 0x0F0F0F0Fu) | (w & 0xF0F0F0F0u) : (w & 0x0F0F0F0Fu) | ((p & 0x0F0F0F0Fu) << 4);
+  const uint32_t r = (uint32_t)__shfl_xor((int)w, 32);
+  return k & 2 ? ((r >> 8) & 0x00FF00FFu) | (w & 0xFF00FF00u) : (w & 0x00FF00FFu) | ((r & 0x00FF00FFu) << 8);
+}
+
+// Bound by memory in the long run, by its four dependent trips (slots, rows,
+// stores) for few tokens. Entries of the list that fill an aligned quad of
+// slots are written whole by the wave that holds the first of them; any other
+// entry's V shares its dwords with tokens that another wave, or an earlier
+// call, owns.
 template <int D, bool F32>
 __global__ __launch_bounds__(256) void k_kv_write(CacheArgs c, const void* k, const void* v, int64_t T, int64_t ks,
                                                   int64_t vs, const int64_t* slots, const float* kg, const float* vg) {
   using R = KvRec<D>;
-  constexpr int kTh = D / 8;
-  const int64_t n = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
-  const int j = (int)(n % kTh);
-  const int64_t th = n / kTh, t = th / c.heads;
-  if (t >= T) return;  // whole groups of kTh lanes
-  const int h = (int)(th - t * c.heads);
-  const int64_t slot = slots[t];
-  const Slot s = slot_at(slot, c.pages, c.page_size);
-  if (!s.ok) return;
-  uint8_t* rec = c.cache + rec_offset<D>(s.page, c.heads, h, c.page_size / 16, s.group);
-  const int64_t col = (int64_t)h * D + 8 * j;
+  const int lane = threadIdx.x & 63, row = lane >> 4;
+  const int64_t first = (((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * 4 + (threadIdx.x >> 6)) * 4;
+  if (first >= T) return;
+  const Unit<D> u = unit_at<D>(blockIdx.x * 16 + (lane & 15), c.heads);
+  // Slots of the entries first - 3 on, one a lane.
+  const int64_t near = first - 3 + (lane & 15);
+  const int64_t s = near >= 0 && near < T && (lane & 15) < 10 ? slots[near] : -2;
+  const int64_t after = __shfl_down(s, 1);
+  const uint32_t runs = (uint32_t)__ballot(after == s + 1);
+  const uint32_t leads = (uint32_t)__ballot(s >= 0 && (s & 3) == 0 && s < c.pages * c.page_size) & runs & (runs >> 1) & (runs >> 2) & 0x7Fu;
+  const int64_t t = first + row;
+  const Slot at = slot_at(__shfl(s, 3 + row), c.pages, c.page_size);
+  const int groups = c.page_size / 16;
   float x[8];
-  uint32_t sc;
-  // K: dword j % (D/32) of lane (j / (D/32), t).
-  load8_at<F32>(k, t * ks + col, x);
-  const uint32_t kc = quant8(x, *kg, sc);
-  const int g = j / (D / 32), blk = j >> 1;
-  *reinterpret_cast<uint32_t*>(rec + g * 16 * R::kLane + s.t * R::kLane + (j % (D / 32)) * 4) = kc;
-  if ((j & 1) == 0) rec[R::kKs + (g * 16 + s.t) * (D / 64) + blk % (D / 64)] = (uint8_t)sc;
-  // V: channel 16 blk + 8 (j & 1) + i, a 16-bit unit per channel and quad.
-  const int role = quad_role(slots, T, t, slot);
-  if (role < 0) return;
-  const int q = s.t >> 2;
-  uint8_t* vrec = rec + R::kV + (q * 16 + 8 * (j & 1)) * R::kLane + 2 * blk;
-  uint8_t* srec = rec + R::kVs + (q * (D / 16) + blk) * 4;
-  if (role == 4) {
-    uint32_t w[4], s4 = 0;
+  if (t < T && at.ok && u.ok) {  // both lanes of a K block
+    load8_at<F32>(k, t * ks + (int64_t)u.h * D + 8 * u.j, x);
+    uint32_t sc;
+    const uint32_t kc = quant8(x, *kg, sc);
+    uint8_t* rec = c.cache + rec_offset<D>(at.page, c.heads, u.h, groups, at.group);
+    const int g = u.j / (D / 32), blk = u.j >> 1;
+    *reinterpret_cast<uint32_t*>(rec + (g * 16 + at.t) * R::kLane + (u.j % (D / 32)) * 4) = kc;
+    if ((u.j & 1) == 0) rec[R::kKs + (g * 16 + at.t) * (D / 64) + blk % (D / 64)] = (uint8_t)sc;
+  }
+  auto load_v = [&](int64_t entry) {
+    const int64_t from = entry * vs + (int64_t)u.h * D + 32 * u.m + 4 * u.c4;
+    load4_at<F32>(v, from, x);
+    load4_at<F32>(v, from + 16, x + 4);
+  };
+  uint32_t sc[2];
+  if ((leads >> 3) & 15u) {  // a quad's first entry is one of the wave's
+    const int lead = __builtin_ctz(leads >> 3);
+    const Slot q = slot_at(__shfl(s, 3 + lead), c.pages, c.page_size);
+    if (u.ok) {
+      load_v(first + lead + row);
+      const uint32_t w = quad_transpose(quant44(x, *vg, sc), row);
+      uint8_t* rec = c.cache + rec_offset<D>(q.page, c.heads, u.h, groups, q.group);
+      *reinterpret_cast<uint32_t*>(rec + v_at<D>(u, q.t >> 2) + row * R::kLane) = w;
+      if (u.c4 < 2) rec[vs_at<D>(u, q.t >> 2) + 4 * u.c4 + row] = (uint8_t)sc[u.c4];
+    }
+  }
+  const bool alone = ((leads >> row) & 15u) == 0;  // none of the quads that could hold entry t is whole
+  if (alone && t < T && at.ok && u.ok) {
+    load_v(t);
+    const uint32_t w = quant44(x, *vg, sc);
+    uint8_t* rec = c.cache + rec_offset<D>(at.page, c.heads, u.h, groups, at.group);
+    // Another entry of this call may own the dword's other nibbles: change
+    // this token's alone. Its old value is stable (no one else writes it), so
+    // xor with old ^ new sets it whatever happens to the rest.
+    const int sh = 4 * (at.t & 3);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      load8_at<F32>(v, (t + i) * vs + col, x);
-      w[i] = quant8(x, *vg, sc);
-      s4 |= sc << (8 * i);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t u = ((w[0] >> 4 * i) & 15u) | (((w[1] >> 4 * i) & 15u) << 4) | (((w[2] >> 4 * i) & 15u) << 8) |
-                         (((w[3] >> 4 * i) & 15u) << 12);
-      *reinterpret_cast<uint16_t*>(vrec + i * R::kLane) = (uint16_t)u;
-    }
-    if ((j & 1) == 0) *reinterpret_cast<uint32_t*>(srec) = s4;
-  } else {
-    load8_at<F32>(v, t * vs + col, x);
-    const uint32_t w = quant8(x, *vg, sc);
-    // Another entry of this call may own the unit's other nibbles: change
-    // this token's alone. Its old value is stable (no one else writes it), so
-    // xor with old ^ new sets it whatever happens to the rest of the dword.
-    const int sh = 16 * (blk & 1) + 4 * (s.t & 3);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t* p = reinterpret_cast<uint32_t*>(reinterpret_cast<uintptr_t>(vrec + i * R::kLane) & ~uintptr_t(3));
+      uint32_t* p = reinterpret_cast<uint32_t*>(rec + v_at<D>(u, at.t >> 2) + i * R::kLane);
       const uint32_t old = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      const uint32_t flip = (((old >> sh) ^ (w >> 4 * i)) & 15u) << sh;
+      const uint32_t flip = (((old >> sh) ^ (w >> 4 * i)) & 0x000F000Fu) << sh;
       if (flip) __hip_atomic_fetch_xor(p, flip, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    if ((j & 1) == 0) srec[s.t & 3] = (uint8_t)sc;
+    if (u.c4 < 2) rec[vs_at<D>(u, at.t >> 2) + 4 * u.c4 + (at.t & 3)] = (uint8_t)sc[u.c4];
   }
 }
 
-// 8 numbers of a code dword with one block scale: fl(fl(q s) g).
-__device__ __forceinline__ void deq8(uint32_t w, float s, float g, float (&y)[8]) {
+// 8 numbers of a code dword: fl(fl(q s) g).
+__device__ __forceinline__ void deq8(uint32_t w, const float (&s)[8], float g, float (&y)[8]) {
   const f32x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0), p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
   const f32x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2), p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
-  y[0] = p0[0] * s * g; y[1] = p0[1] * s * g; y[2] = p1[0] * s * g; y[3] = p1[1] * s * g;
-  y[4] = p2[0] * s * g; y[5] = p2[1] * s * g; y[6] = p3[0] * s * g; y[7] = p3[1] * s * g;
+  const float q[8] = {p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = q[i] * s[i] * g;
 }
 
-// One thread per (list entry, head, 8 channels).
+template <bool F32>
+__device__ __forceinline__ void store4_at(void* base, int64_t elem, const float* v) {
+  if constexpr (F32) {
+    *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(base) + elem) = f32x4{v[0], v[1], v[2], v[3]};
+  } else {
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    *reinterpret_cast<bf16x4*>(reinterpret_cast<__bf16*>(base) + elem) =
+        bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+  }
+}
+
+// Units as in k_kv_write: the four entries of a wave, neighbours in a record
+// as a rule, read the same V dwords.
 template <int D, bool F32>
 __global__ __launch_bounds__(256) void k_kv_read(CacheArgs c, const int64_t* slots, int64_t T, const float* kg,
                                                  const float* vg, void* k, void* v) {
   using R = KvRec<D>;
-  constexpr int kTh = D / 8;
-  const int64_t n = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
-  const int j = (int)(n % kTh);
-  const int64_t th = n / kTh, t = th / c.heads;
-  if (t >= T) return;
-  const int h = (int)(th - t * c.heads);
-  const int64_t slot = slots[t];
-  const Slot s = slot_at(slot, c.pages, c.page_size);
-  const int64_t row = (int64_t)c.heads * D, col = (int64_t)h * D + 8 * j;
-  float y[8];
-  if (!s.ok) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * 4 + (threadIdx.x >> 6)) * 4 + (lane >> 4);
+  const Unit<D> u = unit_at<D>(blockIdx.x * 16 + (lane & 15), c.heads);
+  if (t >= T || !u.ok) return;
+  const Slot at = slot_at(slots[t], c.pages, c.page_size);
+  const int64_t to = t * c.heads * D + (int64_t)u.h * D;
+  float y[8], z[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = 0.0f;
-    store8_at<F32>(k, t * row + col, y);
-    store8_at<F32>(v, t * row + col, y);
-    return;
-  }
-  const uint8_t* rec = c.cache + rec_offset<D>(s.page, c.heads, h, c.page_size / 16, s.group);
-  const int g = j / (D / 32), blk = j >> 1;
-  const uint32_t kc = *reinterpret_cast<const uint32_t*>(rec + g * 16 * R::kLane + s.t * R::kLane + (j % (D / 32)) * 4);
-  const uint32_t ksc = rec[R::kKs + (g * 16 + s.t) * (D / 64) + blk % (D / 64)];
-  deq8(kc, e4m3_to_f32<0>(ksc), *kg, y);
-  store8_at<F32>(k, t * row + col, y);
-  const int role = quad_role(slots, T, t, slot);
-  if (role < 0) return;
-  const int q = s.t >> 2;
-  const uint8_t* vrec = rec + R::kV + (q * 16 + 8 * (j & 1)) * R::kLane + 2 * blk;
-  const uint32_t s4 = *reinterpret_cast<const uint32_t*>(rec + R::kVs + (q * (D / 16) + blk) * 4);
-  uint32_t u[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) u[i] = *reinterpret_cast<const uint16_t*>(vrec + i * R::kLane);
-  const int lo = role == 4 ? 0 : s.t & 3, hi = role == 4 ? 4 : lo + 1;
-  for (int i = lo; i < hi; ++i) {
+  for (int i = 0; i < 8; ++i) y[i] = z[i] = 0.0f;
+  if (at.ok) {
+    const uint8_t* rec = c.cache + rec_offset<D>(at.page, c.heads, u.h, c.page_size / 16, at.group);
+    const int g = u.j / (D / 32), blk = u.j >> 1, sh = 4 * (at.t & 3);
+    const uint32_t kc = *reinterpret_cast<const uint32_t*>(rec + (g * 16 + at.t) * R::kLane + (u.j % (D / 32)) * 4);
+    const uint32_t ksc = rec[R::kKs + (g * 16 + at.t) * (D / 64) + blk % (D / 64)];
+    const u32x2 vsc = *reinterpret_cast<const u32x2*>(rec + vs_at<D>(u, at.t >> 2));
     uint32_t w = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w |= ((u[e] >> 4 * i) & 15u) << 4 * e;
-    deq8(w, e4m3_to_f32<0>((s4 >> 8 * i) & 255u), *vg, y);
-    store8_at<F32>(v, (t + i - lo) * row + col, y);
+    for (int i = 0; i < 4; ++i)
+      w |= ((*reinterpret_cast<const uint32_t*>(rec + v_at<D>(u, at.t >> 2) + i * R::kLane) >> sh) & 0x000F000Fu) << 4 * i;
+    const float vs0 = e4m3_to_f32<0>(vsc[0] >> 2 * sh), vs1 = e4m3_to_f32<0>(vsc[1] >> 2 * sh);
+    const float s[8] = {vs0, vs0, vs0, vs0, vs1, vs1, vs1, vs1};
+    const float ks = e4m3_to_f32<0>(ksc);
+    const float s2[8] = {ks, ks, ks, ks, ks, ks, ks, ks};
+    deq8(kc, s2, *kg, y);
+    deq8(w, s, *vg, z);
   }
+  store8_at<F32>(k, to + 8 * u.j, y);
+  store4_at<F32>(v, to + 32 * u.m + 4 * u.c4, z);
+  store4_at<F32>(v, to + 32 * u.m + 16 + 4 * u.c4, z + 4);
 }
 
-dim3 flat_grid(int64_t threads) {
-  const int64_t wg = (threads + 255) / 256, gx = wg < (1 << 20) ? wg : (1 << 20);
-  return dim3((unsigned)gx, (unsigned)((wg + gx - 1) / gx));
+// x: 16 units of an entry; y, z: 16 entries.
+dim3 unit_grid(int64_t T, int heads, int dim) {
+  const int64_t n = (T + 15) / 16, gy = n < 32768 ? n : 32768;
+  return dim3((unsigned)((heads * (dim / 8) + 15) / 16), (unsigned)gy, (unsigned)((n + gy - 1) / gy));
 }
 
 template <int D>
 void write_d(const CacheArgs& c, const void* k, const void* v, bool f32, int64_t T, int64_t ks, int64_t vs,
              const int64_t* slots, const float* kg, const float* vg, hipStream_t s) {
-  const dim3 grid = flat_grid(T * c.heads * (D / 8));
+  const dim3 grid = unit_grid(T, c.heads, D);
   if (f32) k_kv_write<D, true><<<grid, dim3(256), 0, s>>>(c, k, v, T, ks, vs, slots, kg, vg);
   else k_kv_write<D, false><<<grid, dim3(256), 0, s>>>(c, k, v, T, ks, vs, slots, kg, vg);
 }
 template <int D>
 void read_d(const CacheArgs& c, const int64_t* slots, int64_t T, const float* kg, const float* vg, void* k, void* v,
             bool f32, hipStream_t s) {
-  const dim3 grid = flat_grid(T * c.heads * (D / 8));
+  const dim3 grid = unit_grid(T, c.heads, D);
   if (f32) k_kv_read<D, true><<<grid, dim3(256), 0, s>>>(c, slots, T, kg, vg, k, v);
   else k_kv_read<D, false><<<grid, dim3(256), 0, s>>>(c, slots, T, kg, vg, k, v);
 }
