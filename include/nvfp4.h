@@ -491,7 +491,7 @@ int nvfp4_kv_read(const void* cache, int64_t pages, int64_t page_size, int64_t h
  * most max_q queries of a sequence are computed and its length is clamped to
  * max_len and to the table's width. Keys whose table entry is not a page of
  * the cache are not read and count as hidden. Entries past a sequence's length
- * are not read.
+ * may hold anything.
  * Products run on the f16 matrix core with fp32 accumulation: the cache's
  * values are exact in f16, probabilities round to 11 bits, sums and the
  * softmax statistics are fp32. The result does not depend on the order in

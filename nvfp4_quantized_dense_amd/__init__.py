@@ -122,12 +122,14 @@ def _stream(stream):
     return int(stream)
 
 
+_DTYPE_CODES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+
+
 def _dtype_code(dt):
-    if dt == torch.bfloat16:
-        return DTYPE_BF16
-    if dt == torch.float32:
-        return DTYPE_F32
-    raise ValueError(f"unsupported dtype {dt}")
+    code = _DTYPE_CODES.get(dt)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dt}")
+    return code
 
 
 def _dense(t, name):
@@ -402,58 +404,62 @@ def nvfp4_grouped_gemm(mode, a, a_scales, w_packed, N, K, alpha, masked_m=None, 
 
 
 def _norm_outputs(x, w, residual, residual_out, codes, scales):
-    _dense(x, "x"); _dense(w, "w")
     M, K = x.shape
     if w.numel() != K:
         raise ValueError(f"w must have {K} elements")
-    if residual is not None and (_dense(residual, "residual").shape != x.shape):
+    z = x if residual is None else residual
+    if residual is not None and residual.shape != x.shape:
         raise ValueError("residual must have x's shape")
     if residual_out is None:
-        residual_out = torch.empty_like(x if residual is None else residual)
-    elif residual_out.shape != x.shape or residual_out.dtype != (x if residual is None else residual).dtype:
+        residual_out = torch.empty_like(z)
+    elif residual_out.shape != x.shape or residual_out.dtype != z.dtype:
         raise ValueError("residual_out must have the residual's shape and type")
-    _dense(residual_out, "residual_out")
+    if not (x.is_contiguous() and w.is_contiguous() and z.is_contiguous() and residual_out.is_contiguous()):
+        raise ValueError("x, w, residual and residual_out must be contiguous")
     if codes is None:
-        codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+        codes = x.new_empty((M, K // 2), dtype=torch.uint8)
     if scales is None:
-        scales = torch.empty((M, K // 16), dtype=torch.uint8, device=x.device)
-    return M, K, residual_out, codes, scales
+        scales = x.new_empty((M, K // 16), dtype=torch.uint8)
+    return M, K, _dtype_code(z.dtype), residual_out, codes, scales
 
 
 def add_rmsnorm_nvfp4_quant(x, w, g_inv, residual=None, eps=1e-6, residual_out=None, codes=None, scales=None, stream=None):
     """z = x + residual, y = RMSnorm(z) * w, NVFP4(y) with g_inv: x [M, K] and residual bf16 or f32
     (residual None: z = x), w [K] -> (codes [M, K/2], scales [M, K/16], z). residual_out may be residual."""
-    M, K, residual_out, codes, scales = _norm_outputs(x, w, residual, residual_out, codes, scales)
-    rd = _dtype_code((x if residual is None else residual).dtype)
+    M, K, rd, residual_out, codes, scales = _norm_outputs(x, w, residual, residual_out, codes, scales)
     _check("add_rmsnorm_nvfp4_quant",
-           lib().add_rmsnorm_nvfp4_quant(_ptr(x), _dtype_code(x.dtype), _ptr(residual), rd, _ptr(w), _dtype_code(w.dtype),
-                                         float(eps), M, K, _ptr(g_inv), _ptr(residual_out), _ptr(codes), _ptr(scales),
-                                         _stream(stream)))
+           lib().add_rmsnorm_nvfp4_quant(x.data_ptr(), _dtype_code(x.dtype), _ptr(residual), rd, w.data_ptr(),
+                                         _dtype_code(w.dtype), eps, M, K, _ptr(g_inv), residual_out.data_ptr(),
+                                         codes.data_ptr(), scales.data_ptr(), _stream(stream)))
     return codes, scales, residual_out
 
 
 def add_rmsnorm_nvfp4_quant_per_token(x, w, residual=None, eps=1e-6, residual_out=None, codes=None, scales=None,
                                       row_g=None, stream=None):
     """add_rmsnorm_nvfp4_quant with each row's own global scale -> (codes, scales, z, row_g fp32 [M])."""
-    M, K, residual_out, codes, scales = _norm_outputs(x, w, residual, residual_out, codes, scales)
-    rd = _dtype_code((x if residual is None else residual).dtype)
+    M, K, rd, residual_out, codes, scales = _norm_outputs(x, w, residual, residual_out, codes, scales)
     if row_g is None:
-        row_g = torch.empty(M, dtype=torch.float32, device=x.device)
+        row_g = x.new_empty(M, dtype=torch.float32)
     _check("add_rmsnorm_nvfp4_quant_per_token",
-           lib().add_rmsnorm_nvfp4_quant_per_token(_ptr(x), _dtype_code(x.dtype), _ptr(residual), rd, _ptr(w),
-                                                   _dtype_code(w.dtype), float(eps), M, K, _ptr(residual_out), _ptr(codes),
-                                                   _ptr(scales), _ptr(row_g), _stream(stream)))
+           lib().add_rmsnorm_nvfp4_quant_per_token(x.data_ptr(), _dtype_code(x.dtype), _ptr(residual), rd, w.data_ptr(),
+                                                   _dtype_code(w.dtype), eps, M, K, residual_out.data_ptr(),
+                                                   codes.data_ptr(), scales.data_ptr(), row_g.data_ptr(), _stream(stream)))
     return codes, scales, residual_out, row_g
 
 
 def nvfp4_dequantize(codes, scales, g=None, row_g=None, out=None, out_dtype=torch.bfloat16, stream=None):
     """The numbers of codes [M, K/2] and scales [M, K/16] under the global scale g (1 element) or row_g [M]."""
     _dense(codes, "codes"); _dense(scales, "scales")
-    M, K = codes.shape[0], codes.shape[1] * 2
+    M, K = codes.shape
+    K *= 2
     if out is None:
-        out = torch.empty((M, K), dtype=out_dtype, device=codes.device)
-    _check("nvfp4_dequantize", lib().nvfp4_dequantize(_ptr(codes), _ptr(scales), M, K, _ptr(g), _ptr(row_g), _ptr(out),
-                                                      _dtype_code(out.dtype), _stream(stream)))
+        out = codes.new_empty((M, K), dtype=out_dtype)
+    elif out.numel() != M * K or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous, [{M}, {K}]")
+    if scales.numel() * 16 != M * K:
+        raise ValueError(f"scales must be [{M}, {K // 16}]")
+    _check("nvfp4_dequantize", lib().nvfp4_dequantize(codes.data_ptr(), scales.data_ptr(), M, K, _ptr(g), _ptr(row_g),
+                                                      out.data_ptr(), _dtype_code(out.dtype), _stream(stream)))
     return out
 
 
@@ -470,24 +476,30 @@ def nvfp4_kv_cache(pages, page_size, heads, head_dim, device=None):
 
 def _cache_sizes(cache):
     """(pages, page_size, heads, head_dim) of a cache tensor."""
-    if cache.dim() != 4 or cache.dtype != torch.uint8 or cache.shape[3] % 18:
+    shape = cache.shape
+    if len(shape) != 4 or cache.dtype != torch.uint8 or shape[3] % 18:
         raise ValueError("cache must be uint8 [pages, heads, page_size / 16, 18 * head_dim]")
-    _dense(cache, "cache")
-    return cache.shape[0], 16 * cache.shape[2], cache.shape[1], cache.shape[3] // 18
+    if not cache.is_contiguous():
+        raise ValueError("cache must be contiguous")
+    return shape[0], 16 * shape[2], shape[1], shape[3] // 18
 
 
 def _token_rows(t, name, heads, dim):
-    """Token stride of t [T, heads, dim], whose heads and channels must be dense."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+    """(tokens, token stride) of t [tokens, heads, dim], whose heads and channels must be dense."""
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError(f"{name} must be [tokens, {heads}, {dim}]")
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+    T = shape[0]
+    row, head, channel = t.stride()
+    if T and (channel != 1 or (heads > 1 and head != dim)):
         raise ValueError(f"{name}: heads and channels must be dense")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    return T, row if T > 1 else heads * dim
 
 
-def _whole(t, name, dtype):
-    if t is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}")
+def _list(t, name, dtype):
+    """t, checked to be a dense tensor of dtype."""
+    if t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype}")
     return t
 
 
@@ -495,37 +507,38 @@ def nvfp4_kv_write(k, v, slots, k_g_inv, v_g_inv, cache, stream=None):
     """Quantizes k, v [T, heads, head_dim] (token stride free) into the cache's slots (int64 [T];
     page * page_size + place, outside the cache: skipped). Returns the cache."""
     pages, page_size, heads, dim = _cache_sizes(cache)
-    ks, vs = _token_rows(k, "k", heads, dim), _token_rows(v, "v", heads, dim)
-    _dense(_whole(slots, "slots", torch.int64), "slots")
-    if k.dtype != v.dtype or v.shape[0] != k.shape[0] or slots.numel() != k.shape[0]:
+    T, ks = _token_rows(k, "k", heads, dim)
+    Tv, vs = _token_rows(v, "v", heads, dim)
+    if k.dtype != v.dtype or T != Tv or _list(slots, "slots", torch.int64).numel() != T:
         raise ValueError("k, v and slots must have one type and length")
     _check("nvfp4_kv_write",
-           lib().nvfp4_kv_write(_ptr(k), _ptr(v), _dtype_code(k.dtype), k.shape[0], ks, vs, _ptr(slots), _ptr(k_g_inv),
-                                _ptr(v_g_inv), _ptr(cache), pages, page_size, heads, dim, _stream(stream)))
+           lib().nvfp4_kv_write(k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype), T, ks, vs, slots.data_ptr(),
+                                _ptr(k_g_inv), _ptr(v_g_inv), cache.data_ptr(), pages, page_size, heads, dim,
+                                _stream(stream)))
     return cache
 
 
 def nvfp4_kv_read(cache, slots, k_g, v_g, k=None, v=None, dtype=torch.bfloat16, stream=None):
     """The cache's numbers at slots (int64 [T]) -> (k, v) [T, heads, head_dim], zeros for slots outside it."""
     pages, page_size, heads, dim = _cache_sizes(cache)
-    _dense(_whole(slots, "slots", torch.int64), "slots")
-    shape = (slots.numel(), heads, dim)
+    T = _list(slots, "slots", torch.int64).numel()
+    shape = (T, heads, dim)
     if k is None:
-        k = torch.empty(shape, dtype=dtype, device=cache.device)
+        k = cache.new_empty(shape, dtype=dtype)
+    elif k.shape != shape or not k.is_contiguous():
+        raise ValueError(f"k must be contiguous, {shape}")
     if v is None:
-        v = torch.empty(shape, dtype=k.dtype, device=cache.device)
-    if k.dtype != v.dtype or k.shape != shape or v.shape != shape:
-        raise ValueError(f"k and v must have one type and shape {shape}")
-    _dense(k, "k"); _dense(v, "v")
+        v = k.new_empty(shape)
+    elif v.shape != shape or v.dtype != k.dtype or not v.is_contiguous():
+        raise ValueError(f"v must be contiguous, {shape}, of k's type")
     _check("nvfp4_kv_read",
-           lib().nvfp4_kv_read(_ptr(cache), pages, page_size, heads, dim, _ptr(slots), slots.numel(), _ptr(k_g), _ptr(v_g),
-                               _ptr(k), _ptr(v), _dtype_code(k.dtype), _stream(stream)))
+           lib().nvfp4_kv_read(cache.data_ptr(), pages, page_size, heads, dim, slots.data_ptr(), T, _ptr(k_g), _ptr(v_g),
+                               k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype), _stream(stream)))
     return k, v
 
 
 def nvfp4_kv_attention_workspace_bytes(T, B, heads_q, heads, head_dim, max_q, max_len) -> int:
-    return int(lib().nvfp4_kv_attention_workspace_bytes(int(T), int(B), int(heads_q), int(heads), int(head_dim),
-                                                        int(max_q), int(max_len)))
+    return lib().nvfp4_kv_attention_workspace_bytes(T, B, heads_q, heads, head_dim, max_q, max_len)
 
 
 ATTENTION_COUNTER_BYTES = 4096
@@ -540,18 +553,21 @@ def nvfp4_kv_attention(q, cache, block_table, seq_lens, k_g, v_g, q_offsets=None
     T / B or T, and the table's width). scale: 1 / sqrt(head_dim) by default; window: visible keys of a query (0: all).
     ws: workspace whose first 4096 bytes are zero the first time; allocated if None. Returns out (and lse)."""
     pages, page_size, heads, dim = _cache_sizes(cache)
-    if q.dim() != 3 or q.dtype != torch.bfloat16:
+    shape = q.shape
+    if len(shape) != 3 or q.dtype != torch.bfloat16:
         raise ValueError("q must be bf16 [tokens, heads_q, head_dim]")
-    T, heads_q = q.shape[0], q.shape[1]
-    qs = _token_rows(q, "q", heads_q, dim)
-    B = seq_lens.numel()
-    _dense(_whole(seq_lens, "seq_lens", torch.int32), "seq_lens")
-    _whole(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != B or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be int32 [sequences, width] with dense rows")
-    if q_offsets is not None and _dense(_whole(q_offsets, "q_offsets", torch.int32), "q_offsets").numel() != B + 1:
+    heads_q = shape[1]
+    T, qs = _token_rows(q, "q", heads_q, dim)
+    B = _list(seq_lens, "seq_lens", torch.int32).numel()
+    table = block_table.shape
+    if len(table) != 2 or block_table.dtype != torch.int32 or table[0] != B:
+        raise ValueError("block_table must be int32 [sequences, width]")
+    width = table[1]
+    table_stride, entry = block_table.stride()
+    if width > 1 and entry != 1:
+        raise ValueError("block_table must have dense rows")
+    if q_offsets is not None and _list(q_offsets, "q_offsets", torch.int32).numel() != B + 1:
         raise ValueError("q_offsets must have one more element than seq_lens")
-    width = block_table.shape[1]
     if max_q is None:
         max_q = T if q_offsets is not None else (T // B if B else 0)
     if max_len is None:
@@ -559,21 +575,21 @@ def nvfp4_kv_attention(q, cache, block_table, seq_lens, k_g, v_g, q_offsets=None
     if scale is None:
         scale = dim ** -0.5
     if out is None:
-        out = torch.empty((T, heads_q, dim), dtype=out_dtype, device=q.device)
-    elif _dense(out, "out").shape != q.shape:
-        raise ValueError("out must have q's shape")
-    if lse is None and return_lse:
-        lse = torch.empty((T, heads_q), dtype=torch.float32, device=q.device)
-    elif lse is not None and _dense(_whole(lse, "lse", torch.float32), "lse").numel() != T * heads_q:
+        out = q.new_empty(shape, dtype=out_dtype)
+    elif out.shape != shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous, of q's shape")
+    if lse is None:
+        if return_lse:
+            lse = q.new_empty((T, heads_q), dtype=torch.float32)
+    elif _list(lse, "lse", torch.float32).numel() != T * heads_q:
         raise ValueError("lse must be fp32 [tokens, heads_q]")
     if ws is None:
         n = nvfp4_kv_attention_workspace_bytes(T, B, heads_q, heads, dim, max_q, max_len)
-        ws = torch.empty(max(n, ATTENTION_COUNTER_BYTES), dtype=torch.uint8, device=q.device)
+        ws = q.new_empty(max(n, ATTENTION_COUNTER_BYTES), dtype=torch.uint8)
         ws[:ATTENTION_COUNTER_BYTES].zero_()
     _check("nvfp4_kv_attention",
-           lib().nvfp4_kv_attention(_ptr(q), qs, T, B, heads_q, _ptr(q_offsets), max_q, _ptr(cache), pages, page_size,
-                                    heads, dim, _ptr(block_table), block_table.stride(0) if B > 1 else width, width,
-                                    _ptr(seq_lens), max_len, float(scale), window, _ptr(k_g), _ptr(v_g), _ptr(ws),
-                                    ws.numel() * ws.element_size(), _ptr(out), _dtype_code(out.dtype), _ptr(lse),
-                                    _stream(stream)))
-    return (out, lse) if return_lse or lse is not None else out
+           lib().nvfp4_kv_attention(q.data_ptr(), qs, T, B, heads_q, _ptr(q_offsets), max_q, cache.data_ptr(), pages,
+                                    page_size, heads, dim, block_table.data_ptr(), table_stride if B > 1 else width, width,
+                                    seq_lens.data_ptr(), max_len, scale, window, _ptr(k_g), _ptr(v_g), ws.data_ptr(),
+                                    ws.nbytes, out.data_ptr(), _dtype_code(out.dtype), _ptr(lse), _stream(stream)))
+    return out if lse is None else (out, lse)

@@ -71,6 +71,7 @@ struct AttnPlan {
   bool tiled;           // kv_attention_tile.hip, else kv_attention.hip
   int row_tiles;        // 16-row tiles per workgroup, tiled: per wave
   int64_t units;        // row_blocks * B * heads
+  int rows;             // of a workgroup
   int row_blocks;       // per (sequence, head)
   int chunk;            // keys per split
   int splits;           // most splits of one unit
@@ -82,7 +83,5 @@ hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t
 // kv_attention_tile.hip
 hipError_t launch_kv_attention_tile(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
 constexpr int attn_tile_max(int dim) { return dim == 64 ? 4 : 2; }  // most row tiles of a wave
-// (split, row) pairs that kv_attention.hip's join of a split unit holds in LDS.
-constexpr int kStreamJoin = 4096;
 
 }  // namespace nvfp4

@@ -12,6 +12,10 @@
 namespace nvfp4 {
 namespace {
 
+// More splits of a unit than this are joined by a kernel of their own: one
+// workgroup takes 16 partials of its rows in one trip.
+constexpr int kJoinHere = 16;
+
 #if defined(__HIP_DEVICE_COMPILE__)
 template <int D, int RT, int Y>
 __device__ __forceinline__ void pv(f32x4 (&o)[RT][D / 16], const VFrag<D> (&f)[2], const f16x4 (&vs)[2], const f16x8 (&pf)[RT]) {
@@ -38,10 +42,11 @@ __device__ __forceinline__ bool split_last(uint32_t* counter, int active, uint32
   return true;
 }
 
-// Joins the splits of a unit in split order, so that the result does not
-// depend on which workgroup arrived last. lds: 2 kStreamJoin floats. What
-// this costs is trips to device scope: the first 16 partials of a thread's
-// four channels are asked for together with the statistics.
+// Joins the at most kJoinHere splits of a unit in split order, so that the
+// result does not depend on which workgroup arrived last. What this costs is
+// trips to device scope: partials are asked for together with the statistics.
+// (The loop over batches is run once; written without it the compiler unrolls
+// more, and one token of 64 sequences of up to 8192 keys takes 82 us, not 75.)
 template <int D, int kRows>
 __device__ __forceinline__ void join_splits(const AttnArgs& a, const AttnPlan& p, const Seq& seq, unsigned unit, int active,
                                             int row0, int h, int G, float* lds) {
@@ -60,7 +65,7 @@ __device__ __forceinline__ void join_splits(const AttnArgs& a, const AttnPlan& p
   };
   load(threadIdx.x, 0);
   float* jm = lds;  // [active][kRows] m, then l
-  float* jl = lds + kStreamJoin;
+  float* jl = lds + kJoinHere * kRows;
   for (int n = threadIdx.x; n < active * kRows; n += 256) {
     const uint32_t at = (uint32_t)((n / kRows * p.part_floats + n % kRows) * 4);
     jm[n] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(ra, (int)at, 0, 16));
@@ -92,7 +97,7 @@ __device__ __forceinline__ void join_splits(const AttnArgs& a, const AttnPlan& p
 
 // Workgroups per CU that the registers are held to.
 template <int D, int RT>
-constexpr int kAttnWgs = D == 256 ? 1 : RT == 2 ? 2 : D == 64 ? 4 : 3;
+constexpr int kAttnWgs = D == 256 ? 3 - RT : RT == 2 ? 2 : D == 64 ? 4 : 3;
 
 template <int D, int RT>
 __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArgs a, AttnPlan p) {
@@ -107,6 +112,9 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
   const unsigned rb = unit / heads % blocks, b = unit / heads / blocks;
   const int split = blockIdx.y;
 
+  // Without a window the page numbers of this split can be asked for before
+  // the lengths are known.
+  Walk<D> walk(a, b, h, a.window > 0 ? 0 : split * (p.chunk / 16), lane);
   const Seq seq = seq_of(a, b, G);
   if ((int64_t)rb * kRows >= seq.rows) return;
   const int row0 = (int)rb * kRows;
@@ -115,10 +123,8 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
   const int hi_full = sees_hi(seq, row0 / G), lo_full = sees_lo(hi_all, a.window);  // [lo_full, hi_full) need no mask
   if (split >= active) return;
 
-  Rows<D, RT> r;
-  load_rows<D, RT>(r, a, seq, row0, h, G, quad, col);
-
-  // This wave's stretch, whole steps of 32 tokens.
+  // This wave's stretch, whole steps of 32 tokens. Its first records are asked
+  // for before the query rows.
   const int s_first = all.start + split * p.chunk;
   const int s_last = hi_all - s_first > p.chunk ? s_first + p.chunk : hi_all;
   const int steps = s_last > s_first ? (s_last - s_first + 31) / 32 : 0, per = (steps + 3) / 4;
@@ -129,6 +135,22 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
     VFrag<D> v[2];
     bool ok[2];
   };
+  auto fetch = [&](Pair& f) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint8_t* rec = walk.record(f.ok[x], lane);
+      load_k(f.k[x], rec, lane);
+      load_v(f.v[x], rec, lane, 0);
+      walk.step(1);
+    }
+  };
+  Pair fa, fb;
+  if (step0 < step1) {
+    walk.start((s_first >> 4) + 2 * step0);
+    fetch(fa);
+  }
+  Rows<D, RT> r;
+  load_rows<D, RT>(r, a, seq, row0, h, G, quad, col);
   auto attend = [&](Pair& f, int base) {
     const bool edge = base + 32 > hi_full || base < lo_full || !f.ok[0] || !f.ok[1];
     f32x4 sc[RT][2];
@@ -160,20 +182,8 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
     const f16x4 vs[2] = {e4m3x4_f16(f.v[0].s), e4m3x4_f16(f.v[1].s)};
     pv<D, RT, 0>(r.o, f.v, vs, pf);
   };
+  // The next step's records are on their way while one is computed.
   if (step0 < step1) {
-    // The next step's records are on their way while one is computed.
-    Pair fa, fb;
-    Walk<D> walk(a, b, h, (s_first >> 4) + 2 * step0, (hi_all - 1) >> 4, lane);
-    auto fetch = [&](Pair& f) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint8_t* rec = walk.record(f.ok[x], lane);
-        load_k(f.k[x], rec, lane);
-        load_v(f.v[x], rec, lane, 0);
-        walk.step(1);
-      }
-    };
-    fetch(fa);
     for (int st = step0; st < step1; st += 2) {
       const int base = s_first + 32 * st;
       if (st + 1 < step1) fetch(fb);
@@ -187,7 +197,7 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
 
   // The four waves' results become one: weights exp2(m_w - m) per row.
   __shared__ float wm[4][kRows], wl[4][kRows];
-  __shared__ f32x4 lds[4 * kB * 64 > kStreamJoin / 2 ? 4 * kB * 64 : kStreamJoin / 2];
+  __shared__ f32x4 lds[4 * kB * 64];
   auto wo = [&](int w, int y) -> f32x4& { return lds[(w * kB + y) * 64 + lane]; };
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
@@ -231,18 +241,96 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
       }
     }
   }
-  if (active == 1) return;
+  if (active == 1 || p.splits > kJoinHere) return;
   __shared__ uint32_t arrived;
   if (!split_last(a.counters + unit, active, &arrived)) return;
   join_splits<D, kRows>(a, p, seq, unit, active, row0, h, G, reinterpret_cast<float*>(lds));
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
+// The join of split units by a kernel of its own: 1024 / D / kSlices rows a
+// workgroup, a thread four channels of every kSlices-th run of kRun splits. In
+// the order of the runs, whatever the timing. In one workgroup a unit (the
+// last to arrive) it took 64 rows 5 us a split; so, spread over the chip and
+// with 8 loads in flight a thread, about 5 us in all.
 template <int D>
-void launch_d(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+__global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, AttnPlan p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int kSlices = 4, kRun = 8, kThreads = D / 4, kRowsHere = 256 / kThreads / kSlices;
+  const int G = a.heads_q / a.c.heads, rows_wg = p.rows;
+  const unsigned unit = blockIdx.x, heads = a.c.heads, blocks = p.row_blocks;
+  const int h = (int)(unit % heads);
+  const unsigned rb = p.tiled ? blocks - 1 - unit / heads % blocks : unit / heads % blocks, b = unit / heads / blocks;
+  const Seq seq = seq_of(a, b, G);
+  const int slot = threadIdx.x / kThreads, slice = slot % kSlices, d = threadIdx.x % kThreads * 4;
+  const int rr = blockIdx.y * kRowsHere + slot / kSlices;
+  if ((int64_t)rb * rows_wg + blockIdx.y * kRowsHere >= seq.rows) return;
+  const int row0 = (int)rb * rows_wg;
+  const int active = active_splits(a, p, seq, row0, rows_wg, G).splits;
+  if (active == 1) return;
+  const float* part = a.part + (int64_t)unit * p.splits * p.part_floats;
+  float m = kNoKey, l = 0.0f;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if (row0 + rr < seq.rows) {
+    for (int s0 = slice * kRun; s0 < active; s0 += kSlices * kRun) {
+      float pm[kRun], pl[kRun];
+      f32x4 px[kRun];
+#pragma unroll
+      for (int e = 0; e < kRun; ++e) {
+        const int s = s0 + e < active ? s0 + e : active - 1;
+        const float* ps = part + (int64_t)s * p.part_floats;
+        pm[e] = ps[rr];
+        pl[e] = ps[rows_wg + rr];
+        px[e] = *reinterpret_cast<const f32x4*>(ps + 2 * rows_wg + rr * D + d);
+      }
+      float mn = m;
+#pragma unroll
+      for (int e = 0; e < kRun; ++e) mn = __builtin_fmaxf(mn, pm[e]);
+      const float alpha = __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      l *= alpha;
+      v *= alpha;
+#pragma unroll
+      for (int e = 0; e < kRun; ++e) {
+        const float w = s0 + e < active ? __builtin_amdgcn_exp2f(pm[e] - m) : 0.0f;
+        l += w * pl[e];
+        v += px[e] * w;
+      }
+    }
+  }
+  __shared__ f32x4 jv[256];
+  __shared__ float jm[256], jl[256];
+  jm[threadIdx.x] = m;
+  jl[threadIdx.x] = l;
+  jv[threadIdx.x] = v;
+  __syncthreads();
+  if (slice != 0 || row0 + rr >= seq.rows) return;
+#pragma unroll
+  for (int z = 1; z < kSlices; ++z) m = __builtin_fmaxf(m, jm[threadIdx.x + z * kThreads]);
+  l = 0.0f;
+  v = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int z = 0; z < kSlices; ++z) {
+    const int at = threadIdx.x + z * kThreads;
+    const float w = __builtin_amdgcn_exp2f(jm[at] - m);
+    l += w * jl[at];
+    v += jv[at] * w;
+  }
+  const int64_t orow = out_row(a, seq, row0 + rr, h, G);
+  store4(a, orow * D + d, v * inverse_sum(l, *a.v_g));
+  if (d == 0 && a.lse != nullptr) a.lse[orow] = lse_of(m, l);
+#endif
+}
+
+template <int D>
+void launch_stream(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
   const dim3 grid((unsigned)p.units, (unsigned)p.splits);
   if (p.row_tiles == 1) k_kv_attention<D, 1><<<grid, dim3(256), 0, s>>>(a, p);
   else k_kv_attention<D, 2><<<grid, dim3(256), 0, s>>>(a, p);
+}
+template <int D>
+void launch_join(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+  k_kv_join<D><<<dim3((unsigned)p.units, (unsigned)(p.rows * D / 256)), dim3(256), 0, s>>>(a, p);
 }
 
 }  // namespace
@@ -250,11 +338,10 @@ void launch_d(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
 AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t max_q, int64_t max_len, int64_t window) {
   AttnPlan p{};
   const int64_t rows = max_q * (heads_q / heads);
-  int64_t per, slots, most_splits;  // rows of a workgroup, workgroups that fill the chip
-  p.tiled = rows > 32;
+  int64_t per, slots;  // rows of a workgroup, workgroups that fill the chip
+  p.tiled = rows > 64;
   if (p.tiled) {
     slots = dim == 256 ? 256 : 512;
-    most_splits = 256;
     const int64_t most = 64 * attn_tile_max(dim);
     int64_t blocks = (rows + most - 1) / most;
     if (blocks * B * heads < slots && max_len <= 2048) blocks = (rows + 63) / 64;
@@ -264,7 +351,6 @@ AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t max_q, in
     p.row_tiles = rows <= 16 ? 1 : 2;
     per = 16 * p.row_tiles;
     slots = 1024;
-    most_splits = kStreamJoin / per;
   }
   const int64_t blocks = (rows + per - 1) / per;
   p.units = blocks * B * heads;
@@ -276,24 +362,38 @@ AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t max_q, in
   span = (span + 31) / 32 * 32;
   int64_t want = p.units > 0 ? (slots + p.units - 1) / p.units : 1;
   int64_t bound = want;
-  int64_t most = (span + 255) / 256;  // at least 256 keys each
-  if (most > most_splits) most = most_splits;
+  // At least 512 keys each: 4 sequences of 8000 keys 21.1 us so, 28 with 256
+  // (16 heads of 128 a kv head).
+  int64_t most = (span + 511) / 512;
+  if (most > 256) most = 256;
   if (want > most) want = most;
   if (want < 1) want = 1;
-  if (bound > (max_len + 255) / 256) bound = (max_len + 255) / 256;
+  if (bound > (max_len + 511) / 512) bound = (max_len + 511) / 512;
   p.splits_bound = bound < 1 ? 1 : bound;
   p.chunk = (int)(((span + want - 1) / want + 127) / 128 * 128);
   if (p.chunk < 128) p.chunk = 128;
   p.splits = span > 0 ? (int)((span + p.chunk - 1) / p.chunk) : 1;
+  p.rows = (int)per;
   p.part_floats = (int)per * (dim + 2);
   return p;
 }
 
 hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
-  if (p.tiled) return launch_kv_attention_tile(a, p, s);
-  if (a.c.dim == 64) launch_d<64>(a, p, s);
-  else if (a.c.dim == 128) launch_d<128>(a, p, s);
-  else launch_d<256>(a, p, s);
+  if (p.tiled) {
+    const hipError_t e = launch_kv_attention_tile(a, p, s);
+    if (e != hipSuccess) return e;
+  } else if (a.c.dim == 64) {
+    launch_stream<64>(a, p, s);
+  } else if (a.c.dim == 128) {
+    launch_stream<128>(a, p, s);
+  } else {
+    launch_stream<256>(a, p, s);
+  }
+  if (p.splits > (p.tiled ? 1 : kJoinHere)) {
+    if (a.c.dim == 64) launch_join<64>(a, p, s);
+    else if (a.c.dim == 128) launch_join<128>(a, p, s);
+    else launch_join<256>(a, p, s);
+  }
   return hipGetLastError();
 }
 

@@ -128,9 +128,9 @@ __device__ __forceinline__ f16x8 v_operand(const VFrag<D, PARTS> (&f)[2], const 
 
 // The records of head h in the pages of a block table row, one after the
 // other: where record (page slot ps, group `in`) is. 64 page numbers, of the
-// slots from tab0 on, are in the lanes of `tab`; slots past `last` stand for
-// that one (its keys are masked). A page number outside the cache makes `ok`
-// false and the address that of page 0.
+// slots from tab0 on, are in the lanes of `tab`; slots past the table's last
+// stand for that one. A page number outside the cache (as may stand past a
+// sequence's length) makes `ok` false and the address that of page 0.
 template <int D>
 struct Walk {
   const int32_t* table;
@@ -140,26 +140,31 @@ struct Walk {
   int groups, last, ps, in, tab0, tab;
   __device__ __forceinline__ void load_tab(int lane) {
     const int at = tab0 + lane;
-    tab = table[at < last ? at : last];
-    asm volatile("" : "+v"(tab));  // waits here, not at each use for all loads in flight
+    if (last >= 0) tab = table[at < last ? at : last];
   }
-  // From group g on, the last key's group being g_last.
-  __device__ __forceinline__ Walk(const AttnArgs& a, unsigned b, int h, int g, int g_last, int lane) {
+  // The table from group g on.
+  __device__ __forceinline__ Walk(const AttnArgs& a, unsigned b, int h, int g, int lane) {
     groups = a.c.page_size / 16;
     table = a.table + (int64_t)b * a.table_stride;
     base = a.c.cache + (uint64_t)h * groups * KvRec<D>::kBytes;
     page_bytes = (uint64_t)a.c.heads * groups * KvRec<D>::kBytes;
     pages = (unsigned)a.c.pages;
-    last = g_last / groups;
+    last = (int)a.table_width - 1;
+    ps = tab0 = g / groups;
+    tab = -1;
+    load_tab(lane);
+  }
+  // Records from group g on.
+  __device__ __forceinline__ void start(int g) {
     ps = g / groups;
     in = g - ps * groups;
-    tab0 = ps;
-    load_tab(lane);
+    asm volatile("" : "+v"(tab));  // waits here, not at each use for all loads in flight
   }
   __device__ __forceinline__ const uint8_t* record(bool& ok, int lane) {
     if (ps - tab0 >= 64) {
       tab0 = ps;
       load_tab(lane);
+      asm volatile("" : "+v"(tab));
     }
     const unsigned page = (unsigned)__builtin_amdgcn_readlane(tab, ps - tab0);
     ok = page < pages;

@@ -161,7 +161,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
     if (lane == 0) page_ok[buf][wave] = ok[half];
   };
   if (tiles > 0) {
-    Walk<D> walk(a, b, h, (s_first >> 4) + 2 * pair, (hi_all - 1) >> 4, lane);
+    Walk<D> walk(a, b, h, s_first >> 4, lane);
+    walk.start((s_first >> 4) + 2 * pair);
     auto fetch = [&] {
       const uint8_t* rec[2];
       rec[0] = walk.record(ok[0], lane);
@@ -239,46 +240,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
-// The join of split units, in split order: 1024 / D rows a workgroup, four
-// channels a thread. In one workgroup a unit (the last to arrive) it took 5 us
-// a split; spread over the chip it takes about 5 us in all.
-template <int D>
-__global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, AttnPlan p) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  const int rows_wg = 64 * p.row_tiles, G = a.heads_q / a.c.heads;
-  const unsigned unit = blockIdx.x, heads = a.c.heads, blocks = p.row_blocks;
-  const int h = (int)(unit % heads);
-  const unsigned rb = blocks - 1 - unit / heads % blocks, b = unit / heads / blocks;
-  const Seq seq = seq_of(a, b, G);
-  const int rr = blockIdx.y * (1024 / D) + threadIdx.x / (D / 4), d = threadIdx.x % (D / 4) * 4;
-  if ((int64_t)rb * rows_wg + rr >= seq.rows) return;
-  const int row0 = (int)rb * rows_wg;
-  const int active = active_splits(a, p, seq, row0, rows_wg, G).splits;
-  if (active == 1) return;
-  const float* part = a.part + (int64_t)unit * p.splits * p.part_floats;
-  float m = kNoKey;
-  for (int s = 0; s < active; ++s) m = __builtin_fmaxf(m, part[(int64_t)s * p.part_floats + rr]);
-  float l = 0.0f;
-  f32x4 v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int s = 0; s < active; ++s) {
-    const float* ps = part + (int64_t)s * p.part_floats;
-    const float w = __builtin_amdgcn_exp2f(ps[rr] - m);
-    l += w * ps[rows_wg + rr];
-    v += *reinterpret_cast<const f32x4*>(ps + 2 * rows_wg + rr * D + d) * w;
-  }
-  const int64_t orow = out_row(a, seq, row0 + rr, h, G);
-  store4(a, orow * D + d, v * inverse_sum(l, *a.v_g));
-  if (d == 0 && a.lse != nullptr) a.lse[orow] = lse_of(m, l);
-#endif
-}
-
 template <int D, int RT>
 void launch_rt(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
   if constexpr (RT <= attn_tile_max(D)) {
     if (p.row_tiles != RT) return launch_rt<D, RT + 1>(a, p, s);
     k_kv_attention_tile<D, RT><<<dim3((unsigned)p.units, (unsigned)p.splits), dim3(256), 0, s>>>(a, p);
-    if (p.splits > 1) k_kv_join<D><<<dim3((unsigned)p.units, (unsigned)(64 * RT * D / 1024)), dim3(256), 0, s>>>(a, p);
   }
 }
 
