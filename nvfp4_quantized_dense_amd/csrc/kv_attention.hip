@@ -350,7 +350,10 @@ AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t max_q, in
   } else {
     p.row_tiles = rows <= 16 ? 1 : 2;
     per = 16 * p.row_tiles;
-    slots = 1024;
+    // Three workgroups a CU fit at D 128; a few more even out sequences of
+    // unlike length, of which there are more the more sequences (4 x 131072
+    // keys: 768 / 1024 122 / 137 us; 16 of up to 32000: 88 / 71 us).
+    slots = (rows + per - 1) / per * B * heads <= 64 ? 768 : 1024;
   }
   const int64_t blocks = (rows + per - 1) / per;
   p.units = blocks * B * heads;

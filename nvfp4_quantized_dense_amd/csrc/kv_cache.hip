@@ -58,13 +58,30 @@ __device__ __forceinline__ void store8_at(void* base, int64_t elem, const float 
   }
 }
 
+// The value of lane ^ 1 and lane ^ 2, ^ 16 and ^ 32, without a trip to LDS. A
+// swap of v with itself gives v and the partner's v in some order.
+__device__ __forceinline__ uint32_t xor1(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true);
+}
+__device__ __forceinline__ uint32_t xor2(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true);
+}
+__device__ __forceinline__ uint32_t xor16(uint32_t v) {
+  const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return p[0] ^ p[1] ^ v;
+}
+__device__ __forceinline__ uint32_t xor32(uint32_t v) {
+  const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return p[0] ^ p[1] ^ v;
+}
+
 // NVFP4 of 8 channels (the neighbouring lane holds the block's other 8), by
 // k_quantize's rule.
 __device__ __forceinline__ uint32_t quant8(const float (&v)[8], float g_inv, uint32_t& scale) {
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  m = max(m, (uint32_t)__shfl_xor((int)m, 1));
+  m = max(m, xor1(m));
   const BlockScale bs = block_scale(__uint_as_float(m), g_inv);
   scale = bs.byte;
   float y[8];
@@ -119,30 +136,32 @@ __device__ __forceinline__ void load4_at(const void* base, int64_t elem, float* 
 }
 
 // Two of V's blocks, 4 channels of each in this lane and the others in the
-// neighbours': 8 codes (block 2 m in the low half) and the scale bytes.
-__device__ __forceinline__ uint32_t quant44(const float (&v)[8], float g_inv, uint32_t (&scale)[2]) {
+// neighbours': 8 codes (block 2 m in the low half). Even lanes compute the
+// first block's scale, odd ones the second's: `scale` is that one's byte.
+__device__ __forceinline__ uint32_t quant44(const float (&v)[8], float g_inv, bool odd, uint32_t& scale) {
+  uint32_t m[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m[i >> 2] = max(m[i >> 2], __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  // Lane pairs hand each other the half that the other one needs.
+  const uint32_t give = odd ? m[0] : m[1];
+  uint32_t top = max(odd ? m[1] : m[0], xor1(give));
+  top = max(top, xor2(top));
+  const BlockScale bs = block_scale(__uint_as_float(top), g_inv);
+  scale = bs.byte;
+  const float other = __uint_as_float(xor1(__float_as_uint(bs.r)));
+  const float r0 = odd ? other : bs.r, r1 = odd ? bs.r : other;
   float y[8];
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(v[4 * x + i]) & 0x7FFFFFFFu);
-    m = max(m, (uint32_t)__shfl_xor((int)m, 1));
-    m = max(m, (uint32_t)__shfl_xor((int)m, 2));
-    const BlockScale bs = block_scale(__uint_as_float(m), g_inv);
-    scale[x] = bs.byte;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[4 * x + i] = v[4 * x + i] * bs.r;
-  }
+  for (int i = 0; i < 8; ++i) y[i] = v[i] * (i < 4 ? r0 : r1);
   return e2m1_pack8(y);
 }
 
 // Row k of four holds the codes of token k of a quad, a nibble a channel;
 // becomes the codes of channel k, a nibble a token (both halves alike).
 __device__ __forceinline__ uint32_t quad_transpose(uint32_t w, int k) {
-  const uint32_t p = (uint32_t)__shfl_xor((int)w, 16);
+  const uint32_t p = xor16(w);
   w = k & 1 ? ((p >> 4) & 0x0F0F0F0Fu) | (w & 0xF0F0F0F0u) : (w & 0x0F0F0F0Fu) | ((p & 0x0F0F0F0Fu) << 4);
-  const uint32_t r = (uint32_t)__shfl_xor((int)w, 32);
+  const uint32_t r = xor32(w);
   return k & 2 ? ((r >> 8) & 0x00FF00FFu) | (w & 0xFF00FF00u) : (w & 0x00FF00FFu) | ((r & 0x00FF00FFu) << 8);
 }
 
@@ -159,18 +178,19 @@ __global__ __launch_bounds__(256) void k_kv_write(CacheArgs c, const void* k, co
   const int64_t first = (((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * 4 + (threadIdx.x >> 6)) * 4;
   if (first >= T) return;
   const Unit<D> u = unit_at<D>(blockIdx.x * 16 + (lane & 15), c.heads);
+  const int64_t t = first + row;
+  // K's row is asked for together with the slots.
+  float x[8];
+  if (t < T && u.ok) load8_at<F32>(k, t * ks + (int64_t)u.h * D + 8 * u.j, x);
   // Slots of the entries first - 3 on, one a lane.
   const int64_t near = first - 3 + (lane & 15);
   const int64_t s = near >= 0 && near < T && (lane & 15) < 10 ? slots[near] : -2;
   const int64_t after = __shfl_down(s, 1);
   const uint32_t runs = (uint32_t)__ballot(after == s + 1);
   const uint32_t leads = (uint32_t)__ballot(s >= 0 && (s & 3) == 0 && s < c.pages * c.page_size) & runs & (runs >> 1) & (runs >> 2) & 0x7Fu;
-  const int64_t t = first + row;
   const Slot at = slot_at(__shfl(s, 3 + row), c.pages, c.page_size);
   const int groups = c.page_size / 16;
-  float x[8];
   if (t < T && at.ok && u.ok) {  // both lanes of a K block
-    load8_at<F32>(k, t * ks + (int64_t)u.h * D + 8 * u.j, x);
     uint32_t sc;
     const uint32_t kc = quant8(x, *kg, sc);
     uint8_t* rec = c.cache + rec_offset<D>(at.page, c.heads, u.h, groups, at.group);
@@ -183,22 +203,22 @@ __global__ __launch_bounds__(256) void k_kv_write(CacheArgs c, const void* k, co
     load4_at<F32>(v, from, x);
     load4_at<F32>(v, from + 16, x + 4);
   };
-  uint32_t sc[2];
+  uint32_t sc;
   if ((leads >> 3) & 15u) {  // a quad's first entry is one of the wave's
     const int lead = __builtin_ctz(leads >> 3);
     const Slot q = slot_at(__shfl(s, 3 + lead), c.pages, c.page_size);
     if (u.ok) {
       load_v(first + lead + row);
-      const uint32_t w = quad_transpose(quant44(x, *vg, sc), row);
+      const uint32_t w = quad_transpose(quant44(x, *vg, u.c4 & 1, sc), row);
       uint8_t* rec = c.cache + rec_offset<D>(q.page, c.heads, u.h, groups, q.group);
       *reinterpret_cast<uint32_t*>(rec + v_at<D>(u, q.t >> 2) + row * R::kLane) = w;
-      if (u.c4 < 2) rec[vs_at<D>(u, q.t >> 2) + 4 * u.c4 + row] = (uint8_t)sc[u.c4];
+      if (u.c4 < 2) rec[vs_at<D>(u, q.t >> 2) + 4 * u.c4 + row] = (uint8_t)sc;
     }
   }
   const bool alone = ((leads >> row) & 15u) == 0;  // none of the quads that could hold entry t is whole
   if (alone && t < T && at.ok && u.ok) {
     load_v(t);
-    const uint32_t w = quant44(x, *vg, sc);
+    const uint32_t w = quant44(x, *vg, u.c4 & 1, sc);
     uint8_t* rec = c.cache + rec_offset<D>(at.page, c.heads, u.h, groups, at.group);
     // Another entry of this call may own the dword's other nibbles: change
     // this token's alone. Its old value is stable (no one else writes it), so
@@ -211,7 +231,7 @@ __global__ __launch_bounds__(256) void k_kv_write(CacheArgs c, const void* k, co
       const uint32_t flip = (((old >> sh) ^ (w >> 4 * i)) & 0x000F000Fu) << sh;
       if (flip) __hip_atomic_fetch_xor(p, flip, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    if (u.c4 < 2) rec[vs_at<D>(u, at.t >> 2) + 4 * u.c4 + (at.t & 3)] = (uint8_t)sc[u.c4];
+    if (u.c4 < 2) rec[vs_at<D>(u, at.t >> 2) + 4 * u.c4 + (at.t & 3)] = (uint8_t)sc;
   }
 }
 
