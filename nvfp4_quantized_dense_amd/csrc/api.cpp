@@ -1171,7 +1171,7 @@ int nvfp4_kv_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64_t B
   if (T == 0 || B == 0 || max_q == 0) { g_err[0] = '\0'; return NVFP4_OK; }
   if (!q_offsets && T != B * max_q)
     return fail(NVFP4_ERR_INVALID_ARG, "without q_offsets T=%lld must be B * max_q = %lld", (long long)T, (long long)(B * max_q));
-  if (!q || !cache || !block_table || !seq_lens || !k_g || !v_g || !out)
+  if (!q || !cache || (!block_table && table_width > 0) || !seq_lens || !k_g || !v_g || !out)
     return fail(NVFP4_ERR_INVALID_ARG, "null pointer argument");
   if (q_stride % 8 != 0 || q_stride < (T > 1 ? heads_q * head_dim : 0) || q_stride > (int64_t(1) << 40))
     return fail(NVFP4_ERR_INVALID_ARG, "q's token stride must be at least heads_q * head_dim and a multiple of 8");
