@@ -435,8 +435,8 @@ int nvfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t M, int
 
 /*
  * Paged NVFP4 cache of one layer's keys and values: `pages` pages of
- * page_size tokens (a multiple of 16, at most 65536) of `heads` heads of
- * head_dim channels (64, 128 or 256). A slot is page * page_size + the
+ * page_size tokens (a multiple of 16, at most 65536; fewer than 2^35 tokens in
+ * all) of `heads` heads (at most 4096) of head_dim channels (64, 128 or 256). A slot is page * page_size + the
  * token's place in its page. Keys and values are quantized in blocks of 16
  * channels; 9/8 byte per (token, head, channel) for both together. Layout:
  * uint8 [pages, heads, page_size / 16, 18 * head_dim], a record per 16 tokens

