@@ -351,7 +351,10 @@ AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t max_q, in
     slots = dim == 256 ? 256 : 512;
     const int64_t most = 64 * attn_tile_max(dim);
     int64_t blocks = (rows + most - 1) / most;
-    if (blocks * B * heads < slots && max_len <= 2048) blocks = (rows + 63) / 64;
+    // Few workgroups: smaller ones, unless their rows pay for the keys' second
+    // making (8 heads, group 8: 16 x 16000 keys 28.2 us with 64 rows, 32.4 with
+    // 128; 128 tokens x 8192 keys 66 and 58 us).
+    if (blocks * B * heads < slots && (max_len <= 2048 || rows <= 512)) blocks = (rows + 63) / 64;
     p.row_tiles = (int)((rows + 64 * blocks - 1) / (64 * blocks));
     per = 64 * p.row_tiles;
   } else {
@@ -372,13 +375,15 @@ AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t max_q, in
   span = (span + 31) / 32 * 32;
   int64_t want = p.units > 0 ? (slots + p.units - 1) / p.units : 1;
   int64_t bound = want;
-  // At least 512 keys each: 4 sequences of 8000 keys 21.1 us so, 28 with 256
-  // (16 heads of 128 a kv head).
-  int64_t most = (span + 511) / 512;
+  // At least 512 keys each: one token of 4 sequences of 8000 keys 15.4 us so,
+  // 21.1 with 256 (16 heads of 128 a kv head). Tiled 256, as a workgroup has
+  // more to do a key (16 tokens of one sequence of 1000 keys 15.2 us, 20.0).
+  const int64_t least = p.tiled ? 256 : 512;
+  int64_t most = (span + least - 1) / least;
   if (most > 256) most = 256;
   if (want > most) want = most;
   if (want < 1) want = 1;
-  if (bound > (max_len + 511) / 512) bound = (max_len + 511) / 512;
+  if (bound > (max_len + least - 1) / least) bound = (max_len + least - 1) / least;
   p.splits_bound = bound < 1 ? 1 : bound;
   p.chunk = (int)(((span + want - 1) / want + 127) / 128 * 128);
   if (p.chunk < 128) p.chunk = 128;
