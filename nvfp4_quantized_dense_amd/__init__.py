@@ -403,6 +403,10 @@ def nvfp4_grouped_gemm(mode, a, a_scales, w_packed, N, K, alpha, masked_m=None, 
     return out
 
 
+def _not_on_gpu():
+    raise ValueError("all tensors must be on the GPU")
+
+
 def _norm_outputs(x, w, residual, residual_out, codes, scales):
     M, K = x.shape
     if w.numel() != K:
@@ -418,8 +422,14 @@ def _norm_outputs(x, w, residual, residual_out, codes, scales):
         raise ValueError("x, w, residual and residual_out must be contiguous")
     if codes is None:
         codes = x.new_empty((M, K // 2), dtype=torch.uint8)
+    elif codes.nbytes != M * (K // 2) or not codes.is_contiguous():
+        raise ValueError(f"codes must be contiguous, uint8 [{M}, {K // 2}]")
     if scales is None:
         scales = x.new_empty((M, K // 16), dtype=torch.uint8)
+    elif scales.nbytes != M * (K // 16) or not scales.is_contiguous():
+        raise ValueError(f"scales must be contiguous, uint8 [{M}, {K // 16}]")
+    if not (x.is_cuda and w.is_cuda and z.is_cuda and residual_out.is_cuda and codes.is_cuda and scales.is_cuda):
+        _not_on_gpu()
     return M, K, _dtype_code(z.dtype), residual_out, codes, scales
 
 
@@ -427,6 +437,8 @@ def add_rmsnorm_nvfp4_quant(x, w, g_inv, residual=None, eps=1e-6, residual_out=N
     """z = x + residual, y = RMSnorm(z) * w, NVFP4(y) with g_inv: x [M, K] and residual bf16 or f32
     (residual None: z = x), w [K] -> (codes [M, K/2], scales [M, K/16], z). residual_out may be residual."""
     M, K, rd, residual_out, codes, scales = _norm_outputs(x, w, residual, residual_out, codes, scales)
+    if not g_inv.is_cuda:
+        _not_on_gpu()
     _check("add_rmsnorm_nvfp4_quant",
            lib().add_rmsnorm_nvfp4_quant(x.data_ptr(), _dtype_code(x.dtype), _ptr(residual), rd, w.data_ptr(),
                                          _dtype_code(w.dtype), eps, M, K, _ptr(g_inv), residual_out.data_ptr(),
@@ -440,6 +452,10 @@ def add_rmsnorm_nvfp4_quant_per_token(x, w, residual=None, eps=1e-6, residual_ou
     M, K, rd, residual_out, codes, scales = _norm_outputs(x, w, residual, residual_out, codes, scales)
     if row_g is None:
         row_g = x.new_empty(M, dtype=torch.float32)
+    elif row_g.numel() != M or row_g.dtype != torch.float32 or not row_g.is_contiguous():
+        raise ValueError(f"row_g must be contiguous, fp32 [{M}]")
+    elif not row_g.is_cuda:
+        _not_on_gpu()
     _check("add_rmsnorm_nvfp4_quant_per_token",
            lib().add_rmsnorm_nvfp4_quant_per_token(x.data_ptr(), _dtype_code(x.dtype), _ptr(residual), rd, w.data_ptr(),
                                                    _dtype_code(w.dtype), eps, M, K, residual_out.data_ptr(),
@@ -458,6 +474,8 @@ def nvfp4_dequantize(codes, scales, g=None, row_g=None, out=None, out_dtype=torc
         raise ValueError(f"out must be contiguous, [{M}, {K}]")
     if scales.numel() * 16 != M * K:
         raise ValueError(f"scales must be [{M}, {K // 16}]")
+    if not (codes.is_cuda and scales.is_cuda and out.is_cuda and (g is None or g.is_cuda) and (row_g is None or row_g.is_cuda)):
+        _not_on_gpu()
     _check("nvfp4_dequantize", lib().nvfp4_dequantize(codes.data_ptr(), scales.data_ptr(), M, K, _ptr(g), _ptr(row_g),
                                                       out.data_ptr(), _dtype_code(out.dtype), _stream(stream)))
     return out
@@ -511,6 +529,8 @@ def nvfp4_kv_write(k, v, slots, k_g_inv, v_g_inv, cache, stream=None):
     Tv, vs = _token_rows(v, "v", heads, dim)
     if k.dtype != v.dtype or T != Tv or _list(slots, "slots", torch.int64).numel() != T:
         raise ValueError("k, v and slots must have one type and length")
+    if not (k.is_cuda and v.is_cuda and slots.is_cuda and k_g_inv.is_cuda and v_g_inv.is_cuda and cache.is_cuda):
+        _not_on_gpu()
     _check("nvfp4_kv_write",
            lib().nvfp4_kv_write(k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype), T, ks, vs, slots.data_ptr(),
                                 _ptr(k_g_inv), _ptr(v_g_inv), cache.data_ptr(), pages, page_size, heads, dim,
@@ -531,6 +551,8 @@ def nvfp4_kv_read(cache, slots, k_g, v_g, k=None, v=None, dtype=torch.bfloat16, 
         v = k.new_empty(shape)
     elif v.shape != shape or v.dtype != k.dtype or not v.is_contiguous():
         raise ValueError(f"v must be contiguous, {shape}, of k's type")
+    if not (k.is_cuda and v.is_cuda and slots.is_cuda and k_g.is_cuda and v_g.is_cuda and cache.is_cuda):
+        _not_on_gpu()
     _check("nvfp4_kv_read",
            lib().nvfp4_kv_read(cache.data_ptr(), pages, page_size, heads, dim, slots.data_ptr(), T, _ptr(k_g), _ptr(v_g),
                                k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype), _stream(stream)))
@@ -583,6 +605,10 @@ def nvfp4_kv_attention(q, cache, block_table, seq_lens, k_g, v_g, q_offsets=None
             lse = q.new_empty((T, heads_q), dtype=torch.float32)
     elif _list(lse, "lse", torch.float32).numel() != T * heads_q:
         raise ValueError("lse must be fp32 [tokens, heads_q]")
+    if not (q.is_cuda and cache.is_cuda and block_table.is_cuda and seq_lens.is_cuda and k_g.is_cuda and v_g.is_cuda and
+            out.is_cuda and (q_offsets is None or q_offsets.is_cuda) and (lse is None or lse.is_cuda) and
+            (ws is None or ws.is_cuda)):
+        _not_on_gpu()
     if ws is None:
         n = nvfp4_kv_attention_workspace_bytes(T, B, heads_q, heads, dim, max_q, max_len)
         ws = q.new_empty(max(n, ATTENTION_COUNTER_BYTES), dtype=torch.uint8)

@@ -56,5 +56,23 @@ def test_binding_outputs():
     for bad in (dict(residual=x[:1]), dict(residual=x, residual_out=x.float()), dict(residual=torch.zeros(2, 128, dtype=torch.bfloat16)[:, :64])):
         with pytest.raises(ValueError):
             nv.add_rmsnorm_nvfp4_quant(x, w, g, **bad)
+    c = torch.zeros(2, 32, dtype=torch.uint8)
+    for bad in (dict(codes=c[:1]), dict(scales=c), dict(row_g=torch.zeros(1)), dict(row_g=torch.zeros(2).double())):
+        with pytest.raises(ValueError, match="must be contiguous"):
+            nv.add_rmsnorm_nvfp4_quant_per_token(x, w, **bad)
     with pytest.raises(ValueError):
         nv.nvfp4_dequantize(torch.zeros(2, 32, dtype=torch.uint8), torch.zeros(2, 3, dtype=torch.uint8), g=g)
+
+
+def test_tensors_on_the_host_are_refused():
+    cache = nv.nvfp4_kv_cache(2, 16, 2, 64)
+    s, g = torch.zeros(3, dtype=torch.int64), torch.ones(1)
+    k, q = torch.zeros(3, 2, 64, dtype=torch.bfloat16), torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    t, n = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    x, w = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(64, dtype=torch.bfloat16)
+    c, sc = torch.zeros(2, 32, dtype=torch.uint8), torch.zeros(2, 4, dtype=torch.uint8)
+    for call in (lambda: nv.nvfp4_kv_write(k, k, s, g, g, cache), lambda: nv.nvfp4_kv_read(cache, s, g, g),
+                 lambda: nv.nvfp4_kv_attention(q, cache, t, n, g, g), lambda: nv.add_rmsnorm_nvfp4_quant(x, w, g),
+                 lambda: nv.add_rmsnorm_nvfp4_quant_per_token(x, w), lambda: nv.nvfp4_dequantize(c, sc, g=g)):
+        with pytest.raises(ValueError, match="on the GPU"):
+            call()
