@@ -449,12 +449,12 @@ def add_rmsnorm_nvfp4_quant(x, w, g_inv, residual=None, eps=1e-6, residual_out=N
 def add_rmsnorm_nvfp4_quant_per_token(x, w, residual=None, eps=1e-6, residual_out=None, codes=None, scales=None,
                                       row_g=None, stream=None):
     """add_rmsnorm_nvfp4_quant with each row's own global scale -> (codes, scales, z, row_g fp32 [M])."""
-    M, K, rd, residual_out, codes, scales = _norm_outputs(x, w, residual, residual_out, codes, scales)
     if row_g is None:
-        row_g = x.new_empty(M, dtype=torch.float32)
-    elif row_g.numel() != M or row_g.dtype != torch.float32 or not row_g.is_contiguous():
-        raise ValueError(f"row_g must be contiguous, fp32 [{M}]")
-    elif not row_g.is_cuda:
+        row_g = x.new_empty(x.shape[0], dtype=torch.float32)
+    elif row_g.numel() != x.shape[0] or row_g.dtype != torch.float32 or not row_g.is_contiguous():
+        raise ValueError(f"row_g must be contiguous, fp32 [{x.shape[0]}]")
+    M, K, rd, residual_out, codes, scales = _norm_outputs(x, w, residual, residual_out, codes, scales)
+    if not row_g.is_cuda:
         _not_on_gpu()
     _check("add_rmsnorm_nvfp4_quant_per_token",
            lib().add_rmsnorm_nvfp4_quant_per_token(x.data_ptr(), _dtype_code(x.dtype), _ptr(residual), rd, w.data_ptr(),
