@@ -145,7 +145,7 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
   auto fetch = [&](Pair& f) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const uint8_t* rec = walk.record(f.ok[x], lane);
+      const Rsrc rec = walk.record(f.ok[x], lane);
       load_k(f.k[x], rec, lane);
       load_v(f.v[x], rec, lane, 0);
       walk.step(1);

@@ -73,35 +73,37 @@ struct VFrag {
   uint32_t c[D / 32 / PARTS], s;
 };
 
+// A record as a buffer: a lane's offset into it is a constant of the kernel, and
+// addresses cost no vector instructions.
 template <int N>
-__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t* p) {
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], Rsrc rec, uint32_t at) {
   if constexpr (N == 1) {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
+    w[0] = __builtin_amdgcn_raw_buffer_load_b32(rec, (int)at, 0, 0);
   } else if constexpr (N == 2) {
-    const u32x2 t = *reinterpret_cast<const u32x2*>(p);
+    const u32x2 t = __builtin_amdgcn_raw_buffer_load_b64(rec, (int)at, 0, 0);
     w[0] = t[0]; w[1] = t[1];
   } else {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-      const u32x4 t = *reinterpret_cast<const u32x4*>(p + 4 * i);
+      const u32x4 t = bload16(rec, at + 4 * i);
       w[i] = t[0]; w[i + 1] = t[1]; w[i + 2] = t[2]; w[i + 3] = t[3];
     }
   }
 }
 
 template <int D>
-__device__ __forceinline__ void load_k(KFrag<D>& f, const uint8_t* rec, unsigned lane) {
-  load_words(f.c, rec + lane * KvRec<D>::kLane);
-  const uint8_t* s = rec + KvRec<D>::kKs + lane * (D / 64);
-  if constexpr (D == 64) f.s = *s;
-  else if constexpr (D == 128) f.s = *reinterpret_cast<const uint16_t*>(s);
-  else f.s = *reinterpret_cast<const uint32_t*>(s);
+__device__ __forceinline__ void load_k(KFrag<D>& f, Rsrc rec, unsigned lane) {
+  load_words(f.c, rec, lane * KvRec<D>::kLane);
+  const int s = KvRec<D>::kKs + lane * (D / 64);
+  if constexpr (D == 64) f.s = __builtin_amdgcn_raw_buffer_load_b8(rec, s, 0, 0);
+  else if constexpr (D == 128) f.s = __builtin_amdgcn_raw_buffer_load_b16(rec, s, 0, 0);
+  else f.s = __builtin_amdgcn_raw_buffer_load_b32(rec, s, 0, 0);
 }
 template <int D, int PARTS>
-__device__ __forceinline__ void load_v(VFrag<D, PARTS>& f, const uint8_t* rec, unsigned lane, unsigned part) {
+__device__ __forceinline__ void load_v(VFrag<D, PARTS>& f, Rsrc rec, unsigned lane, unsigned part) {
   constexpr int kN = D / 16 / PARTS;
-  load_words(f.c, rec + KvRec<D>::kV + lane * KvRec<D>::kLane + part * (2 * kN));
-  f.s = *reinterpret_cast<const uint32_t*>(rec + KvRec<D>::kVs + (lane >> 4) * (D / 4) + (part * kN + (lane & (kN - 1))) * 4);
+  load_words(f.c, rec, KvRec<D>::kV + lane * KvRec<D>::kLane + part * (2 * kN));
+  f.s = __builtin_amdgcn_raw_buffer_load_b32(rec, KvRec<D>::kVs + (lane >> 4) * (D / 4) + (part * kN + (lane & (kN - 1))) * 4, 0, 0);
 }
 
 // Lane N's value in each row of 16 lanes.
@@ -160,7 +162,7 @@ struct Walk {
     in = g - ps * groups;
     asm volatile("" : "+v"(tab));  // waits here, not at each use for all loads in flight
   }
-  __device__ __forceinline__ const uint8_t* record(bool& ok, int lane) {
+  __device__ __forceinline__ Rsrc record(bool& ok, int lane) {
     if (ps - tab0 >= 64) {
       tab0 = ps;
       load_tab(lane);
@@ -168,7 +170,7 @@ struct Walk {
     }
     const unsigned page = (unsigned)__builtin_amdgcn_readlane(tab, ps - tab0);
     ok = page < pages;
-    return base + (ok ? page : 0u) * page_bytes + (unsigned)in * KvRec<D>::kBytes;
+    return make_rsrc(base + (ok ? page : 0u) * page_bytes + (unsigned)in * KvRec<D>::kBytes, KvRec<D>::kBytes);
   }
   __device__ __forceinline__ void step(int by) {
     in += by;

@@ -167,14 +167,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
     Walk<D> walk(a, b, h, s_first >> 4, lane);
     walk.start((s_first >> 4) + 2 * pair);
     auto fetch = [&] {
-      const uint8_t* rec[2];
-      rec[0] = walk.record(ok[0], lane);
-      walk.step(1);
-      rec[1] = walk.record(ok[1], lane);
-      walk.step(3);
-      load_v(fv[0], rec[0], lane, half);
-      load_v(fv[1], rec[1], lane, half);
-      load_k(fk, half ? rec[1] : rec[0], lane);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const Rsrc rec = walk.record(ok[x], lane);
+        load_v(fv[x], rec, lane, half);
+        if (x == half) load_k(fk, rec, lane);
+        walk.step(x == 0 ? 1 : 3);
+      }
     };
     fetch();
     clear_v(s_first);
