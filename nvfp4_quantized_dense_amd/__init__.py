@@ -115,8 +115,9 @@ def _stream(stream):
         if not _gpu:
             if not torch.cuda.is_available():
                 return None
+            torch.cuda.init()
             _gpu = True
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -421,11 +422,11 @@ def _norm_outputs(x, w, residual, residual_out, codes, scales):
     if not (x.is_contiguous() and w.is_contiguous() and z.is_contiguous() and residual_out.is_contiguous()):
         raise ValueError("x, w, residual and residual_out must be contiguous")
     if codes is None:
-        codes = x.new_empty((M, K // 2), dtype=torch.uint8)
+        codes = torch.empty(M, K // 2, dtype=torch.uint8, device=x.device)
     elif codes.nbytes != M * (K // 2) or not codes.is_contiguous():
         raise ValueError(f"codes must be contiguous, uint8 [{M}, {K // 2}]")
     if scales is None:
-        scales = x.new_empty((M, K // 16), dtype=torch.uint8)
+        scales = torch.empty(M, K // 16, dtype=torch.uint8, device=x.device)
     elif scales.nbytes != M * (K // 16) or not scales.is_contiguous():
         raise ValueError(f"scales must be contiguous, uint8 [{M}, {K // 16}]")
     if not (x.is_cuda and w.is_cuda and z.is_cuda and residual_out.is_cuda and codes.is_cuda and scales.is_cuda):
@@ -450,7 +451,7 @@ def add_rmsnorm_nvfp4_quant_per_token(x, w, residual=None, eps=1e-6, residual_ou
                                       row_g=None, stream=None):
     """add_rmsnorm_nvfp4_quant with each row's own global scale -> (codes, scales, z, row_g fp32 [M])."""
     if row_g is None:
-        row_g = x.new_empty(x.shape[0], dtype=torch.float32)
+        row_g = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
     elif row_g.numel() != x.shape[0] or row_g.dtype != torch.float32 or not row_g.is_contiguous():
         raise ValueError(f"row_g must be contiguous, fp32 [{x.shape[0]}]")
     M, K, rd, residual_out, codes, scales = _norm_outputs(x, w, residual, residual_out, codes, scales)
@@ -469,7 +470,7 @@ def nvfp4_dequantize(codes, scales, g=None, row_g=None, out=None, out_dtype=torc
     M, K = codes.shape
     K *= 2
     if out is None:
-        out = codes.new_empty((M, K), dtype=out_dtype)
+        out = torch.empty(M, K, dtype=out_dtype, device=codes.device)
     elif out.numel() != M * K or not out.is_contiguous():
         raise ValueError(f"out must be contiguous, [{M}, {K}]")
     if scales.numel() * 16 != M * K:
@@ -544,11 +545,11 @@ def nvfp4_kv_read(cache, slots, k_g, v_g, k=None, v=None, dtype=torch.bfloat16, 
     T = _list(slots, "slots", torch.int64).numel()
     shape = (T, heads, dim)
     if k is None:
-        k = cache.new_empty(shape, dtype=dtype)
+        k = torch.empty(T, heads, dim, dtype=dtype, device=cache.device)
     elif k.shape != shape or not k.is_contiguous():
         raise ValueError(f"k must be contiguous, {shape}")
     if v is None:
-        v = k.new_empty(shape)
+        v = torch.empty_like(k)
     elif v.shape != shape or v.dtype != k.dtype or not v.is_contiguous():
         raise ValueError(f"v must be contiguous, {shape}, of k's type")
     if not (k.is_cuda and v.is_cuda and slots.is_cuda and k_g.is_cuda and v_g.is_cuda and cache.is_cuda):
@@ -597,12 +598,12 @@ def nvfp4_kv_attention(q, cache, block_table, seq_lens, k_g, v_g, q_offsets=None
     if scale is None:
         scale = dim ** -0.5
     if out is None:
-        out = q.new_empty(shape, dtype=out_dtype)
+        out = torch.empty(T, heads_q, dim, dtype=out_dtype, device=q.device)
     elif out.shape != shape or not out.is_contiguous():
         raise ValueError("out must be contiguous, of q's shape")
     if lse is None:
         if return_lse:
-            lse = q.new_empty((T, heads_q), dtype=torch.float32)
+            lse = torch.empty(T, heads_q, dtype=torch.float32, device=q.device)
     elif _list(lse, "lse", torch.float32).numel() != T * heads_q:
         raise ValueError("lse must be fp32 [tokens, heads_q]")
     if not (q.is_cuda and cache.is_cuda and block_table.is_cuda and seq_lens.is_cuda and k_g.is_cuda and v_g.is_cuda and
@@ -611,7 +612,7 @@ def nvfp4_kv_attention(q, cache, block_table, seq_lens, k_g, v_g, q_offsets=None
         _not_on_gpu()
     if ws is None:
         n = nvfp4_kv_attention_workspace_bytes(T, B, heads_q, heads, dim, max_q, max_len)
-        ws = q.new_empty(max(n, ATTENTION_COUNTER_BYTES), dtype=torch.uint8)
+        ws = torch.empty(max(n, ATTENTION_COUNTER_BYTES), dtype=torch.uint8, device=q.device)
         ws[:ATTENTION_COUNTER_BYTES].zero_()
     _check("nvfp4_kv_attention",
            lib().nvfp4_kv_attention(q.data_ptr(), qs, T, B, heads_q, _ptr(q_offsets), max_q, cache.data_ptr(), pages,
