@@ -27,7 +27,11 @@ namespace {
 
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
-constexpr float kNoKey = -3.0e38f;  // running maximum before the first key
+// The maximum of no key, in units of log2; and of raw scores, below all of
+// them (D <= 256 products of at most 2 and 2688: under 2^21): times a
+// factor it is finite, so that a hidden score of -inf stays -inf.
+constexpr float kNoKey = -3.0e38f;
+constexpr float kNoScore = -0x1p24f;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
 
@@ -264,7 +268,7 @@ __device__ __forceinline__ void load_rows(Rows<D, RT>& r, const AttnArgs& a, con
     const int head = h * G + row - i * G, hi = live ? sees_hi(seq, i) : 0;
     r.lo[t] = sees_lo(hi, a.window);
     r.n[t] = hi - r.lo[t];
-    r.m[t] = r.t[t] = kNoKey;
+    r.m[t] = r.t[t] = kNoScore;
     r.l[t] = 0.0f;
     uint32_t w[kW * 4];
     uint32_t top = 0;
@@ -355,7 +359,7 @@ __device__ __forceinline__ void renew_maximum(Rows<D, RT>& r, const float (&mx)[
       const float mn = mr > r.t[t] ? mr : r.m[t];
       const float alpha = __builtin_amdgcn_exp2f((r.m[t] - mn) * r.f[t]);
       r.m[t] = mn;
-      r.t[t] = mn == kNoKey ? kNoKey : mn + 8.0f / r.f[t];
+      r.t[t] = mn == kNoScore ? kNoScore : mn + 8.0f / r.f[t];
       r.l[t] *= alpha;
 #pragma unroll
       for (int y = 0; y < D / 16; ++y) r.o[t][y] *= alpha;
@@ -386,7 +390,7 @@ __device__ __forceinline__ void finish_rows(Rows<D, RT>& r) {
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     r.l[t] = sum_xor32(sum_xor16(r.l[t]));
-    r.m[t] = r.m[t] == kNoKey ? kNoKey : r.m[t] * r.f[t];
+    r.m[t] = r.m[t] == kNoScore ? kNoKey : r.m[t] * r.f[t];
   }
 }
 

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import nvfp4_quantized_dense_amd as nv
+import test_gpu_kv_attention as base
 from attention_reference import attend, bf16
 from test_gpu_kv_attention import KG, VG, Case, dev
 
@@ -61,6 +62,19 @@ def test_unlike_rows():
     c.q[2] *= 2.0 ** 20
     c.q[3, :, 5] *= 1000
     c.check(*c.run())
+
+
+@pytest.mark.parametrize("n,lens,window", [
+    (3, [34, 1, 0], 1),        # the first pair of groups hidden to some rows; rows of no key
+    (1, [2100, 3], 40), (60, [100, 20, 2500], 7), (60, [2500, 59], 0)])
+@pytest.mark.parametrize("G", [1, 2])
+def test_hidden_under_a_large_factor(n, lens, window, G, monkeypatch):
+    """A global scale of 1 and large queries: steps, waves and splits that are hidden to a row as a whole."""
+    monkeypatch.setattr(base, "KG", np.float32(1))
+    monkeypatch.setattr(base, "KG_INV", np.float32(1))
+    c = Case(lens, [n] * len(lens), G, 1, 64, 16, seed=13)
+    c.q *= 8
+    c.check(*c.run(window=window), window=window)
 
 
 @pytest.mark.parametrize("n", [1, 40])
