@@ -57,7 +57,7 @@ __device__ __forceinline__ void load8_at(const void* base, int64_t elem, float (
 }
 
 // Rows on their way out are stored past the caches (nontemporal): 65536 tokens
-// of 8 heads of 128 took 61 us so, 103 us with plain stores.
+// of 8 heads of 128 took 57 us so, 103 us with plain stores.
 template <bool F32>
 __device__ __forceinline__ void store8_at(void* base, int64_t elem, const float (&v)[8]) {
   if constexpr (F32) {
@@ -181,10 +181,10 @@ __device__ __forceinline__ uint32_t quad_transpose(uint32_t w, int k) {
 
 // 8192 tokens of 8 heads of 128 (43 MB) take 10.9 us, bound by instruction
 // issue (two block scales with their exact divisions a lane) as much as by
-// memory; 64 tokens 3.2 us, the dependent trips: slots, rows, stores. Entries of the list that fill an aligned quad of
-// slots are written whole by the wave that holds the first of them; any other
-// entry's V shares its dwords with tokens that another wave, or an earlier
-// call, owns.
+// memory; 64 tokens 3.8 us, the dependent trips: slots, rows, stores. Entries
+// of the list that fill an aligned quad of slots are written whole by the wave
+// that holds the first of them; any other entry's V shares its dwords with
+// tokens that another wave, or an earlier call, owns.
 template <int D, bool F32>
 __global__ __launch_bounds__(256) void k_kv_write(CacheArgs c, const void* k, const void* v, int64_t T, int64_t ks,
                                                   int64_t vs, const int64_t* slots, const float* kg, const float* vg,
@@ -276,7 +276,7 @@ __device__ __forceinline__ void store4_at(void* base, int64_t elem, const float*
 
 // Units as in k_kv_write: the four entries of a wave, neighbours in a record
 // as a rule, read the same V dwords. Bound by memory: 65536 tokens of 8 heads
-// of 128, 344 MB, in 57 us, 6.0 TB/s (most of it stores).
+// of 128, 344 MB, in 53 us, 6.5 TB/s (most of it stores).
 template <int D, bool F32>
 __global__ __launch_bounds__(256) void k_kv_read(CacheArgs c, const int64_t* slots, int64_t T, const float* kg,
                                                  const float* vg, void* k, void* v, Div groups) {
