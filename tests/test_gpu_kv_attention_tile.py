@@ -100,6 +100,21 @@ def test_many_splits(D, Hq, H, lens):
     assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+@pytest.mark.parametrize("D,Hq,H,n,lens", [(64, 4, 2, 70, [3000, 500]), (128, 4, 1, 150, [2500]), (128, 1, 1, 600, [2600, 700]),
+                                           (256, 2, 1, 90, [1500, 90]), (128, 2, 1, 3, [6000])])
+def test_workspace_of_any_window(D, Hq, H, n, lens):
+    """Splits and row blocks differ by the window; the workspace asked for without one holds for all."""
+    c = Case(lens, [n] * len(lens), Hq, H, D, 64, seed=14)
+    size = nv.nvfp4_kv_attention_workspace_bytes(n * len(lens), len(lens), Hq, H, D, n, c.table.shape[1] * 64)
+    ws = torch.full((size + (32 << 20),), 255, dtype=torch.uint8, device="cuda")
+    ws[:4096] = 0
+    for window in (0, 1, 30, 100, 300, 700, 1300, 2400):
+        o, lse = c.run(ws=ws[:size], window=window)
+        if window in (0, 30, 700):
+            c.check(o, lse, window=window)
+        assert int(ws[size:].min()) == 255 and int(ws[:4096].max()) == 0
+
+
 @pytest.mark.parametrize("n", [1, 30])
 def test_many_pages_a_stretch(n):
     """1024 (sequence, head) pairs leave each key axis whole: 75 pages of 16 tokens in one stretch. The
