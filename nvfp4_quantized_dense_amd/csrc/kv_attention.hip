@@ -403,10 +403,10 @@ AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t max_q, in
     // takes least time by this measure, in units of a tile: the tiles of a
     // workgroup, fewer for earlier queries, and 5 to begin and end, times the
     // rounds (where two share a CU, a last one of half the workgroups takes
-    // 0.6); 8 for the join and 10 for a round's partials. D 128: 70 units of 4
-    // kv heads over 30000 keys 931 / 793 / 616 us with 1 / 2 / 3 splits, 90
-    // over 8192 keys 248 / 251 / 226; 75 of 64 rows over 600 keys 21 / 35 with
-    // 1 / 2.
+    // 0.6); 8 for the join and 10 for a round's partials. D 128, 4 kv heads:
+    // 70 row blocks over 30000 keys 931 / 793 / 616 us with 1 / 2 / 3 splits,
+    // 79 over 8192 keys 248 / 251 / 226; 75 of 64 rows over 600 keys 21 / 35
+    // with 1 / 2.
     const double unseen = 0.5 * (double)max_q / (double)(max_len > max_q ? max_len : max_q);
     const double tiles = (double)((span + 63) / 64) * (window > 0 ? 1.0 : 1.0 - unseen);
     double least_cost = 0.0;
