@@ -484,7 +484,7 @@ int nvfp4_kv_read(const void* cache, int64_t pages, int64_t page_size, int64_t h
  * (window 0: 0 .. p); query head a reads kv head a / (heads_q / heads).
  *   out = sum_j softmax_j(scale * q . k_j) v_j,  lse = log sum_j exp(scale * q . k_j)
  * (natural logarithm, after scaling). A query that sees no key gets out = 0,
- * lse = -inf. q is bf16 with a token stride in elements (a multiple of 8);
+ * lse = -inf, whatever it holds. q is bf16 with a token stride in elements (a multiple of 8);
  * out [T, heads_q, head_dim] of out_dtype; lse fp32 [T, heads_q] or NULL. Rows
  * of q that belong to no sequence are not written.
  * max_q and max_len are host-side bounds of the query counts and lengths: at

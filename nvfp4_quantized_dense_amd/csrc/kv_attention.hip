@@ -209,7 +209,7 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     if (quad == 0) {
-      wm[wave][16 * t + col] = r.m[t];
+      wm[wave][16 * t + col] = row_maximum<D, RT>(r, t);
       wl[wave][16 * t + col] = r.l[t];
     }
   }
@@ -221,7 +221,7 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
   for (int t = 0; t < RT; ++t) {
     const int rr = 16 * t + col;
     const float m = __builtin_fmaxf(__builtin_fmaxf(wm[0][rr], wm[1][rr]), __builtin_fmaxf(wm[2][rr], wm[3][rr]));
-    const float alpha = __builtin_amdgcn_exp2f(r.m[t] - m);
+    const float alpha = __builtin_amdgcn_exp2f(wm[wave][rr] - m);
     float l = 0.0f;
 #pragma unroll
     for (int w = 0; w < 4; ++w) l += wl[w][rr] * __builtin_amdgcn_exp2f(wm[w][rr] - m);

@@ -28,8 +28,7 @@ namespace {
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
 // The maximum of no key, in units of log2; and of raw scores, below all of
-// them (D <= 256 products of at most 2 and 2688: under 2^21): times a
-// factor it is finite, so that a hidden score of -inf stays -inf.
+// them (D <= 256 products of at most 2 and 2688: under 2^21).
 constexpr float kNoKey = -3.0e38f;
 constexpr float kNoScore = -0x1p24f;
 constexpr float kLog2e = 1.44269504088896341f;
@@ -244,14 +243,16 @@ __device__ __forceinline__ Stretch active_splits(const AttnArgs& a, const AttnPl
 }
 
 // RT tiles of 16 rows: lane (quad, col) holds row col of a tile, of its output
-// channels 16 y + 4 quad + [0, 4). m, l: the maximum (of raw scores, factor f
-// to base 2) and the sum so far, the latter over this lane's tokens; t: the
-// raw score above which the maximum is renewed.
+// channels 16 y + 4 quad + [0, 4). A raw score s has the probability
+// exp2(s f + a): -a is the subtracted maximum, in units of log2. l: their sum
+// so far, over this lane's tokens; t: the raw score above which the maximum is
+// renewed, kNoScore before the first key. a is zero until then, so that a
+// hidden score of -inf gives the probability 0 whatever the query holds.
 template <int D, int RT>
 struct Rows {
   f32x4 o[RT][D / 16];
   f16x8 q[RT][D / 32];
-  float m[RT], l[RT], f[RT], t[RT];
+  float a[RT], l[RT], f[RT], t[RT];
   int lo[RT], n[RT];  // keys seen: lo .. lo + n - 1
 };
 
@@ -268,8 +269,8 @@ __device__ __forceinline__ void load_rows(Rows<D, RT>& r, const AttnArgs& a, con
     const int head = h * G + row - i * G, hi = live ? sees_hi(seq, i) : 0;
     r.lo[t] = sees_lo(hi, a.window);
     r.n[t] = hi - r.lo[t];
-    r.m[t] = r.t[t] = kNoScore;
-    r.l[t] = 0.0f;
+    r.t[t] = kNoScore;
+    r.a[t] = r.l[t] = 0.0f;
     uint32_t w[kW * 4];
     uint32_t top = 0;
     if (live) {
@@ -356,10 +357,10 @@ __device__ __forceinline__ void renew_maximum(Rows<D, RT>& r, const float (&mx)[
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       const float mr = max_xor32(max_xor16(mx[t]));
-      const float mn = mr > r.t[t] ? mr : r.m[t];
-      const float alpha = __builtin_amdgcn_exp2f((r.m[t] - mn) * r.f[t]);
-      r.m[t] = mn;
-      r.t[t] = mn == kNoScore ? kNoScore : mn + 8.0f / r.f[t];
+      const float a = mr > r.t[t] ? -mr * r.f[t] : r.a[t];
+      const float alpha = r.t[t] == kNoScore ? 0.0f : __builtin_amdgcn_exp2f(a - r.a[t]);
+      r.t[t] = mr > r.t[t] ? mr + 8.0f / r.f[t] : r.t[t];
+      r.a[t] = a;
       r.l[t] *= alpha;
 #pragma unroll
       for (int y = 0; y < D / 16; ++y) r.o[t][y] *= alpha;
@@ -372,10 +373,9 @@ template <int D, int RT>
 __device__ __forceinline__ void probabilities(Rows<D, RT>& r, const f32x4 (&sc)[RT][2], f16x8 (&pf)[RT]) {
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
-    const float mf = -r.m[t] * r.f[t];
     float e[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][i >> 2][i & 3], r.f[t], mf));
+    for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][i >> 2][i & 3], r.f[t], r.a[t]));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       r.l[t] += e[i];
@@ -384,14 +384,16 @@ __device__ __forceinline__ void probabilities(Rows<D, RT>& r, const f32x4 (&sc)[
   }
 }
 
-// After the last key: sums over all tokens, maxima in units of log2.
+// After the last key: sums over all tokens.
 template <int D, int RT>
 __device__ __forceinline__ void finish_rows(Rows<D, RT>& r) {
 #pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    r.l[t] = sum_xor32(sum_xor16(r.l[t]));
-    r.m[t] = r.m[t] == kNoScore ? kNoKey : r.m[t] * r.f[t];
-  }
+  for (int t = 0; t < RT; ++t) r.l[t] = sum_xor32(sum_xor16(r.l[t]));
+}
+// The subtracted maximum of tile t's rows, in units of log2.
+template <int D, int RT>
+__device__ __forceinline__ float row_maximum(const Rows<D, RT>& r, int t) {
+  return r.t[t] == kNoScore ? kNoKey : -r.a[t];
 }
 
 // ---- results ----------------------------------------------------------------

@@ -107,12 +107,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
     const f16x8 *kp = lds + k0 * 64 + lane, *vp = lds + v0 * 64 + lane;
     f16x8 op[kAhead], pf[RT];
     auto operand = [&](int n) { return n < 2 * kW ? kp[n * 64] : vp[(n - 2 * kW) * 64]; };
-    float mf[RT], e[RT];
+    float e[RT];
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      mf[t] = -r.m[t] * r.f[t];
-      later[t][0] = later[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
+    for (int t = 0; t < RT; ++t) later[t][0] = later[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) op[n] = operand(n);
     static_for<2 * kW>([&](auto step) {
@@ -122,7 +119,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
         later[t][n / kW] = mfma16x16x32(op[n % kAhead], r.q[t][n % kW], later[t][n / kW]);
 #pragma unroll
         for (int i = 8 * n / (2 * kW); i < 8 * (n + 1) / (2 * kW); ++i) {
-          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(now[t][i >> 2][i & 3], r.f[t], mf[t]));
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(now[t][i >> 2][i & 3], r.f[t], r.a[t]));
           r.l[t] += p;
           if (i & 1) { pf[t][i - 1] = (_Float16)e[t]; pf[t][i] = (_Float16)p; }
           e[t] = p;
@@ -228,13 +225,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
       const int64_t orow = out_row(a, seq, row0 + rr, h, G);
 #pragma unroll
       for (int y = 0; y < kB; ++y) store4(a, orow * D + 16 * y + 4 * quad, r.o[t][y] * inv);
-      if (quad == 0 && a.lse != nullptr) a.lse[orow] = lse_of(r.m[t], r.l[t]);
+      if (quad == 0 && a.lse != nullptr) a.lse[orow] = lse_of(row_maximum<D, RT>(r, t), r.l[t]);
     } else {
 #pragma unroll
       for (int y = 0; y < kB; ++y)
         *reinterpret_cast<f32x4*>(part + 2 * kRows + rr * D + 16 * y + 4 * quad) = r.o[t][y];
       if (quad == 0) {
-        part[rr] = r.m[t];
+        part[rr] = row_maximum<D, RT>(r, t);
         part[kRows + rr] = r.l[t];
       }
     }
