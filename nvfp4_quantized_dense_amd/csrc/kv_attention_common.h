@@ -11,8 +11,8 @@
 // [2^-10, 2688], exact in f16. A bf16 query row is scaled by a power of two
 // to at most 1 before it becomes f16: exact but for elements 2^-14 below the
 // row's largest, which are off by 2^-25 of it. Probabilities are rounded to
-// f16 for the second product (half a step 2^-11, or 2^-25 absolute under
-// 2^-14); their sum is kept in fp32. S^T leaves a lane with the tokens of
+// f16 for the second product: half a step 2^-11, or under 2^-21 of the row's
+// largest 2^-32 of that (kUp below); their sum is kept in fp32. S^T leaves a lane with the tokens of
 // one query row that the second product wants from that lane, because the
 // record's V codes are stored in the same token order, so the probabilities
 // never leave their registers, and the row statistics are one number a lane.
@@ -31,6 +31,13 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 // them (D <= 256 products of at most 2 and 2688: under 2^21).
 constexpr float kNoKey = -3.0e38f;
 constexpr float kNoScore = -0x1p24f;
+// Probabilities are computed 2^kUp times as large as they are and may pass the
+// subtracted maximum by 2^kLazy: f16 holds up to 2^16, and has 11 bits down
+// to 2^-14. With 10 and 5.9 (maxima renewed more often) the matrix-bound
+// calls took 1 to 4% longer, with 13 and 2.9 3 to 8%; with 0 and 8 as long,
+// but one key of value 0 that stood 16 above 4096 others (natural logarithm)
+// left their sum 9% off.
+constexpr float kUp = 7.0f, kLazy = 8.0f;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
 
@@ -244,7 +251,8 @@ __device__ __forceinline__ Stretch active_splits(const AttnArgs& a, const AttnPl
 
 // RT tiles of 16 rows: lane (quad, col) holds row col of a tile, of its output
 // channels 16 y + 4 quad + [0, 4). A raw score s has the probability
-// exp2(s f + a): -a is the subtracted maximum, in units of log2. l: their sum
+// exp2(s f + a), 2^kUp times as large as under the subtracted maximum: kUp - a
+// is that, in units of log2. l: their sum
 // so far, over this lane's tokens; t: the raw score above which the maximum is
 // renewed, kNoScore before the first key. a is zero until then, so that a
 // hidden score of -inf gives the probability 0 whatever the query holds.
@@ -345,7 +353,7 @@ __device__ __forceinline__ void lane_maximum(const f32x4 (&sc)[RT][2], float (&m
 }
 
 // mx: the maximum of a pair's scores in this lane. The subtracted maximum
-// follows the true one only when a score passes it by more than 2^8 in
+// follows the true one only when a score passes it by more than 2^kLazy in
 // probability: f16 holds probabilities up to that as exactly as up to 1, and
 // most steps then need neither the exchange between lanes nor the rescaling.
 template <int D, int RT>
@@ -357,9 +365,9 @@ __device__ __forceinline__ void renew_maximum(Rows<D, RT>& r, const float (&mx)[
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       const float mr = max_xor32(max_xor16(mx[t]));
-      const float a = mr > r.t[t] ? -mr * r.f[t] : r.a[t];
+      const float a = mr > r.t[t] ? __builtin_fmaf(-mr, r.f[t], kUp) : r.a[t];
       const float alpha = r.t[t] == kNoScore ? 0.0f : __builtin_amdgcn_exp2f(a - r.a[t]);
-      r.t[t] = mr > r.t[t] ? mr + 8.0f / r.f[t] : r.t[t];
+      r.t[t] = mr > r.t[t] ? mr + kLazy / r.f[t] : r.t[t];
       r.a[t] = a;
       r.l[t] *= alpha;
 #pragma unroll
@@ -390,7 +398,8 @@ __device__ __forceinline__ void finish_rows(Rows<D, RT>& r) {
 #pragma unroll
   for (int t = 0; t < RT; ++t) r.l[t] = sum_xor32(sum_xor16(r.l[t]));
 }
-// The subtracted maximum of tile t's rows, in units of log2.
+// The subtracted maximum of tile t's rows in units of log2, less kUp: what the
+// sum l and the outputs count from.
 template <int D, int RT>
 __device__ __forceinline__ float row_maximum(const Rows<D, RT>& r, int t) {
   return r.t[t] == kNoScore ? kNoKey : -r.a[t];
