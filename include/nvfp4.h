@@ -493,9 +493,9 @@ int nvfp4_kv_read(const void* cache, int64_t pages, int64_t page_size, int64_t h
  * the cache are not read and count as hidden. Entries past a sequence's length
  * may hold anything.
  * Products run on the f16 matrix core with fp32 accumulation: the cache's
- * values are exact in f16, probabilities round to 11 bits down to 2^-21 of
- * the row's largest and to multiples of 2^-31 of it below, sums and the
- * softmax statistics are fp32. The result does not depend on the order in
+ * values are exact in f16, probabilities round to 11 bits (22 if out_dtype
+ * is f32) down to 2^-21 of the row's largest and to multiples of 2^-31 of it
+ * below, sums and the softmax statistics are fp32. The result does not depend on the order in
  * which workgroups finish.
  * ws: nvfp4_kv_attention_workspace_bytes(...) bytes, 16-byte aligned. Its
  * first 4096 bytes (arrival counters of a split key axis) must be zero the

@@ -574,7 +574,8 @@ def nvfp4_kv_attention(q, cache, block_table, seq_lens, k_g, v_g, q_offsets=None
     block_table int32 [B, width], seq_lens int32 [B]; sequence b's queries are q[q_offsets[b]:q_offsets[b + 1]]
     (int32 [B + 1]; None: T / B each) at its last positions; rows of no sequence are not written. max_q, max_len:
     bounds known on the host (default: T / B or T, and the table's width). scale: 1 / sqrt(head_dim) by default; window: visible keys of a query (0: all).
-    ws: workspace whose first 4096 bytes are zero the first time; allocated if None. Returns out (and lse)."""
+    ws: workspace whose first 4096 bytes are zero the first time; allocated if None. out_dtype fp32 computes with
+    probabilities of 22 bits, bf16 with 11. Returns out (and lse)."""
     pages, page_size, heads, dim = _cache_sizes(cache)
     shape = q.shape
     if len(shape) != 3 or q.dtype != torch.bfloat16:

@@ -24,12 +24,15 @@ namespace {
 constexpr int kJoinHere = 16;
 
 #if defined(__HIP_DEVICE_COMPILE__)
-template <int D, int RT, int Y>
-__device__ __forceinline__ void pv(f32x4 (&o)[RT][D / 16], const VFrag<D> (&f)[2], const f16x4 (&vs)[2], const f16x8 (&pf)[RT]) {
+template <int D, int RT, int P, int Y>
+__device__ __forceinline__ void pv(f32x4 (&o)[RT][D / 16], const VFrag<D> (&f)[2], const f16x4 (&vs)[2],
+                                   const f16x8 (&pf)[P][RT]) {
   const f16x8 vf = v_operand<Y>(f, vs);
 #pragma unroll
-  for (int t = 0; t < RT; ++t) o[t][Y] = mfma16x16x32(vf, pf[t], o[t][Y]);
-  if constexpr (Y + 1 < D / 16) pv<D, RT, Y + 1>(o, f, vs, pf);
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int x = 0; x < P; ++x) o[t][Y] = mfma16x16x32(vf, pf[x][t], o[t][Y]);
+  if constexpr (Y + 1 < D / 16) pv<D, RT, P, Y + 1>(o, f, vs, pf);
 }
 #endif
 
@@ -106,7 +109,8 @@ __device__ __forceinline__ void join_splits(const AttnArgs& a, const AttnPlan& p
 template <int D, int RT>
 constexpr int kAttnWgs = D == 256 ? 3 - RT : RT == 2 ? 2 : D == 64 ? 4 : 3;
 
-template <int D, int RT>
+// P: f16 parts of a probability.
+template <int D, int RT, int P>
 __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArgs a, AttnPlan p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int kB = D / 16, kW = D / 32, kRows = 16 * RT;
@@ -181,13 +185,13 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
 #pragma unroll
       for (int x = 0; x < 2; ++x) f.v[x].s &= f.ok[x] ? byte_mask(base + 16 * x + 4 * quad, lo_all, hi_all) : 0u;
     }
-    f16x8 pf[RT];
+    f16x8 pf[P][RT];
     float mx[RT];
     lane_maximum<RT>(sc, mx);
     renew_maximum<D, RT>(r, mx);
-    probabilities<D, RT>(r, sc, pf);
+    probabilities<D, RT, P>(r, sc, pf);
     const f16x4 vs[2] = {e4m3x4_f16(f.v[0].s), e4m3x4_f16(f.v[1].s)};
-    pv<D, RT, 0>(r.o, f.v, vs, pf);
+    pv<D, RT, P, 0>(r.o, f.v, vs, pf);
   };
   // The next step's records are on their way while one is computed.
   if (step0 < step1) {
@@ -329,11 +333,16 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, AttnPlan p) {
 #endif
 }
 
+template <int D, int P>
+void launch_parts(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+  const dim3 grid((unsigned)p.units, (unsigned)p.splits);
+  if (p.row_tiles == 1) k_kv_attention<D, 1, P><<<grid, dim3(256), 0, s>>>(a, p);
+  else k_kv_attention<D, 2, P><<<grid, dim3(256), 0, s>>>(a, p);
+}
 template <int D>
 void launch_stream(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
-  const dim3 grid((unsigned)p.units, (unsigned)p.splits);
-  if (p.row_tiles == 1) k_kv_attention<D, 1><<<grid, dim3(256), 0, s>>>(a, p);
-  else k_kv_attention<D, 2><<<grid, dim3(256), 0, s>>>(a, p);
+  if (a.f32_out) launch_parts<D, 2>(a, p, s);
+  else launch_parts<D, 1>(a, p, s);
 }
 template <int D>
 void launch_join(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {

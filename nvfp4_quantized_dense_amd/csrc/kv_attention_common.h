@@ -12,10 +12,12 @@
 // to at most 1 before it becomes f16: exact but for elements 2^-14 below the
 // row's largest, which are off by 2^-25 of it. Probabilities are rounded to
 // f16 for the second product: half a step 2^-11, or under 2^-21 of the row's
-// largest 2^-32 of that (kUp below); their sum is kept in fp32. S^T leaves a lane with the tokens of
-// one query row that the second product wants from that lane, because the
-// record's V codes are stored in the same token order, so the probabilities
-// never leave their registers, and the row statistics are one number a lane.
+// largest 2^-32 of that (kUp below); that is 1/8 of a bf16 output's own
+// rounding, and f32 outputs take them in two parts, 2^-22. Their sum is kept
+// in fp32. S^T leaves a lane with the tokens of one query row that the second
+// product wants from that lane, because the record's V codes are stored in the
+// same token order, so the probabilities never leave their registers, and the
+// row statistics are one number a lane.
 #pragma once
 #include <type_traits>
 
@@ -376,9 +378,19 @@ __device__ __forceinline__ void renew_maximum(Rows<D, RT>& r, const float (&mx)[
   }
 }
 
+// A probability as P f16 operands: of 11 bits, or of 22 in two parts for f32
+// outputs. The second part costs half as many matrix instructions again and 3
+// vector instructions a probability: 64 sequences of up to 8192 keys 68 / 75
+// us, 4 of 131072 118 / 120, chunks of up to 2047 tokens 451 / 584.
+template <int P, int RT>
+__device__ __forceinline__ void put_probability(f16x8 (&pf)[P][RT], int t, int i, float p) {
+  pf[0][t][i] = (_Float16)p;
+  if constexpr (P == 2) pf[1][t][i] = (_Float16)(p - (float)pf[0][t][i]);
+}
+
 // Probabilities of a pair's scores, as operands.
-template <int D, int RT>
-__device__ __forceinline__ void probabilities(Rows<D, RT>& r, const f32x4 (&sc)[RT][2], f16x8 (&pf)[RT]) {
+template <int D, int RT, int P>
+__device__ __forceinline__ void probabilities(Rows<D, RT>& r, const f32x4 (&sc)[RT][2], f16x8 (&pf)[P][RT]) {
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     float e[8];
@@ -387,7 +399,7 @@ __device__ __forceinline__ void probabilities(Rows<D, RT>& r, const f32x4 (&sc)[
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       r.l[t] += e[i];
-      pf[t][i] = (_Float16)e[i];
+      put_probability(pf, t, i, e[i]);
     }
   }
 }

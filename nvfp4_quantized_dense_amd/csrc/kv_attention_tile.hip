@@ -28,7 +28,8 @@ constexpr int kTile = 64;  // keys
 
 #endif
 
-template <int D, int RT>
+// P: f16 parts of a probability.
+template <int D, int RT, int P>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(AttnArgs a, AttnPlan p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int kB = D / 16, kW = D / 32, kRows = 64 * RT;
@@ -105,7 +106,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
   // order, and few registers alive.
   auto attend = [&](const f32x4 (&now)[RT][2], f32x4 (&later)[RT][2], float (&mx)[RT], int k0, int v0, auto&& make) {
     const f16x8 *kp = lds + k0 * 64 + lane, *vp = lds + v0 * 64 + lane;
-    f16x8 op[kAhead], pf[RT];
+    f16x8 op[kAhead], pf[P][RT];
     auto operand = [&](int n) { return n < 2 * kW ? kp[n * 64] : vp[(n - 2 * kW) * 64]; };
     float e[RT];
 #pragma unroll
@@ -121,7 +122,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
         for (int i = 8 * n / (2 * kW); i < 8 * (n + 1) / (2 * kW); ++i) {
           const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(now[t][i >> 2][i & 3], r.f[t], r.a[t]));
           r.l[t] += p;
-          if (i & 1) { pf[t][i - 1] = (_Float16)e[t]; pf[t][i] = (_Float16)p; }
+          if (i & 1) {
+            put_probability(pf, t, i - 1, e[t]);
+            put_probability(pf, t, i, p);
+          }
           e[t] = p;
         }
       }
@@ -131,7 +135,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
     static_for<kB>([&](auto step) {
       constexpr int y = decltype(step)::value, n = 2 * kW + y;
 #pragma unroll
-      for (int t = 0; t < RT; ++t) r.o[t][y] = mfma16x16x32(op[n % kAhead], pf[t], r.o[t][y]);
+      for (int x = 0; x < P; ++x)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) r.o[t][y] = mfma16x16x32(op[n % kAhead], pf[x][t], r.o[t][y]);
       if constexpr (y + kAhead < kB) op[n % kAhead] = operand(n + kAhead);
       make(step);
       // The next pair's maximum, by lane.
@@ -243,7 +249,9 @@ template <int D, int RT>
 void launch_rt(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
   if constexpr (RT <= attn_tile_max(D)) {
     if (p.row_tiles != RT) return launch_rt<D, RT + 1>(a, p, s);
-    k_kv_attention_tile<D, RT><<<dim3((unsigned)p.units, (unsigned)p.splits), dim3(256), 0, s>>>(a, p);
+    const dim3 grid((unsigned)p.units, (unsigned)p.splits);
+    if (a.f32_out) k_kv_attention_tile<D, RT, 2><<<grid, dim3(256), 0, s>>>(a, p);
+    else k_kv_attention_tile<D, RT, 1><<<grid, dim3(256), 0, s>>>(a, p);
   }
 }
 

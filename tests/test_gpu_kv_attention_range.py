@@ -46,19 +46,18 @@ class Sink(Case):
         self.scale = gap / size
         self.cache = torch.from_numpy(cache).cuda()
 
-    def check_sink(self, o, lse, step, floor):
-        """`step`: half a step of a probability, relative; `floor`: that of the smallest, to the row's largest (a key's
-        error is at most the larger of both)."""
-        q, one = self.q.double().numpy(), [np.abs(v) for v in self.v]
-        ro, rl, eo, el = attend(q, self.k, self.v, self.lens, self.qs, self.scale)
-        mass = attend(q, self.k, one, self.lens, self.qs, self.scale)[0]
-        most = max(float(v.max()) for v in one)
-        eo = eo + (step - 2.0 ** -11) * mass + max(self.lens) * floor * most
-        if o.dtype == torch.bfloat16:
-            eo = eo + 2.0 ** -8 * np.abs(ro)
-        o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
-        assert (np.abs(o - ro) <= eo).all(), (np.abs(o - ro) / ro).max()
-        assert (np.abs(lse - rl) <= el).all()
+def check_bits(c, o, lse, scale, step, floor, window=0):
+    """Case.check with a probability's half step `step`, relative, or `floor` of the row's largest."""
+    q, size = c.q.double().numpy(), [np.abs(v) for v in c.v]
+    ro, rl, eo, el = attend(q, c.k, c.v, c.lens, c.qs, scale, window)
+    mass = attend(q, c.k, size, c.lens, c.qs, scale, window)[0]
+    eo = eo + (step - 2.0 ** -11) * mass + max(c.lens) * floor * max(float(v.max()) for v in size if v.size)
+    if o.dtype == torch.bfloat16:
+        eo = eo + 2.0 ** -8 * np.abs(ro)
+    o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert (np.abs(o - ro) <= eo).all(), (np.abs(o - ro) - eo).max()
+    seen = np.isfinite(rl)
+    assert (np.abs(lse[seen] - rl[seen]) <= el[seen]).all()
 
 
 @pytest.mark.parametrize("gap", [8.0, 14.0, 16.0, 18.0, 22.0])
@@ -66,6 +65,37 @@ class Sink(Case):
     (128, 1, 4, 1, [4096], 0), (64, 1, 2, 1, [3000, 777], 700), (256, 1, 2, 2, [1500], 3),
     (128, 70, 1, 1, [4096], 0), (64, 70, 2, 1, [2500], 1000), (256, 70, 1, 1, [2000, 300], 1)])
 def test_one_key_takes_nearly_all(gap, D, n, Hq, H, lens, at):
-    """The others' values are not lost: probabilities keep 11 bits down to 2^-21 of the largest, and steps of 2^-31 below."""
+    """The others' values are not lost: probabilities keep 11 bits (22 for f32 outputs) down to 2^-21 of the largest, and
+    steps of 2^-31 below."""
     c = Sink(lens, n, Hq, H, D, 64, at, gap, seed=D + n)
-    c.check_sink(*c.run(scale=c.scale, out_dtype=torch.bfloat16), 2.0 ** -11, 2.0 ** -32)
+    check_bits(c, *c.run(scale=c.scale, out_dtype=torch.bfloat16), c.scale, 2.0 ** -11, 2.0 ** -32)
+    check_bits(c, *c.run(scale=c.scale), c.scale, 2.0 ** -22, 2.0 ** -32)
+
+
+@pytest.mark.parametrize("D,Hq,H,n,lens,window", [
+    (128, 4, 1, 1, [3000, 1, 70], 0), (64, 10, 2, 1, [130, 900], 0), (256, 20, 1, 1, [1300, 9], 0), (128, 8, 1, 1, [9000], 0),
+    (128, 6, 2, 8, [300, 8, 5], 40), (256, 8, 1, 4, [200], 0), (128, 5, 1, 40, [1500, 41], 0), (64, 4, 1, 64, [2200], 0),
+    (64, 8, 2, 30, [500], 100), (256, 3, 1, 40, [700], 0)])
+def test_f32_output(D, Hq, H, n, lens, window):
+    c = Case(lens, [n] * len(lens), Hq, H, D, 32, seed=D + n)
+    o, lse = c.run(window=window)
+    check_bits(c, o, lse, D ** -0.5, 2.0 ** -22, 2.0 ** -32, window)
+
+
+@pytest.mark.parametrize("D,n,lens", [(64, 1, [2, 3, 9]), (128, 1, [5, 2]), (256, 3, [4, 9]), (64, 70, [70]), (128, 80, [81]), (256, 70, [70])])
+def test_f32_output_has_more_than_11_bits(D, n, lens):
+    """Queries of one channel: scores are single products, exact, so that a probability's own roundings show: f's and the
+    exponent's (each half a step 2^-24 of a score up to 2^3 in size, as attend counts them) and its two parts."""
+    c = Case(lens, [n] * len(lens), 1, 1, D, 16, seed=n + D)
+    c.q[:, :, :5] = 0
+    c.q[:, :, 6:] = 0
+    c.v = [np.abs(v) for v in c.v]
+    c.cache[..., 8 * D:16 * D] &= 0x77
+    o = c.run()[0].double().cpu().numpy()
+    for b, L in enumerate(lens):
+        for i in range(n):
+            s = c.k[b][:L - n + i + 1, 0, 5] * float(c.q[b * n + i, 0, 5]) * D ** -0.5
+            w, v = np.exp(s - s.max()), c.v[b][:len(s), 0]
+            ref = w @ v / w.sum()
+            far = 2.0 ** -22 + 2.0 ** -24 * (16 * (np.abs(s).max() + abs(s.max())) + 16 + 2 * (L / 32 + 64))
+            assert (np.abs(o[b * n + i, 0] - ref) <= far * ref + (2.0 ** -24 + L * 2.0 ** -32) * v.max()).all(), (b, i)
