@@ -6,6 +6,7 @@ Argument marshalling only: every step of the path runs in the HIP library
 built (``python -m nvfp4_quantized_dense_amd.build``); importing this module
 without it fails loudly, there is no other implementation.
 """
+import contextlib
 import ctypes
 import os
 
@@ -121,6 +122,16 @@ def _stream(stream):
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _on(stream):
+    """Context in which torch allocates and fills what a call on `stream` uses: on the stream itself, so that the
+    kernel comes after the fill, and the memory, once released, goes to work that comes after the kernel."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
 
 
 _DTYPE_CODES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
@@ -291,10 +302,15 @@ def silu_mul_nvfp4_quant(gate_up, g_inv, masked_m=None, codes=None, scales=None,
     gu = gate_up if gate_up.dim() == 3 else gate_up.unsqueeze(0)
     E, M, I2 = gu.shape
     I = I2 // 2
+    # The caller's outputs are of the current stream; the kernel's is the one that clears them.
     if codes is None:
-        codes = torch.zeros((E, M, I // 2), dtype=torch.uint8, device=gu.device)
+        codes = torch.empty((E, M, I // 2), dtype=torch.uint8, device=gu.device)
+        with _on(stream):
+            codes.zero_()
     if scales is None:
-        scales = torch.zeros((E, M, I // 16), dtype=torch.uint8, device=gu.device)
+        scales = torch.empty((E, M, I // 16), dtype=torch.uint8, device=gu.device)
+        with _on(stream):
+            scales.zero_()
     _check("silu_mul_nvfp4_quant",
            lib().silu_mul_nvfp4_quant(_ptr(gu), E, M, I, _ptr(masked_m), _ptr(g_inv), _ptr(codes), _ptr(scales),
                                       _stream(stream)))
@@ -332,7 +348,8 @@ def mlp_forward(mode, x, w_gu_packed, alpha_gu, w_d_packed, alpha_d, I, g1_inv=N
     M, H = x.shape
     nws = mlp_workspace_bytes(mode, M, H, I)
     if ws is None:
-        ws = torch.zeros(max(nws, 1), dtype=torch.uint8, device=x.device)
+        with _on(stream):
+            ws = torch.zeros(max(nws, 1), dtype=torch.uint8, device=x.device)
     if out is None:
         out = torch.empty((M, H), dtype=out_dtype, device=x.device)
     _check("mlp_forward", lib().mlp_forward(int(mode), _ptr(x), M, H, I, _ptr(w_gu_packed), _ptr(alpha_gu),
@@ -378,7 +395,8 @@ def mlp_forward_w4a16_awq(x, w_gu_packed, g_gu, s_gu, w_d_packed, g_d, s_d, I, w
     M, H = x.shape
     nws = mlp_workspace_bytes(MODE_W4A16_AWQ, M, H, I)
     if ws is None:
-        ws = torch.zeros(max(nws, 1), dtype=torch.uint8, device=x.device)
+        with _on(stream):
+            ws = torch.zeros(max(nws, 1), dtype=torch.uint8, device=x.device)
     if out is None:
         out = torch.empty((M, H), dtype=out_dtype, device=x.device)
     _check("mlp_forward_w4a16_awq",
@@ -613,8 +631,9 @@ def nvfp4_kv_attention(q, cache, block_table, seq_lens, k_g, v_g, q_offsets=None
         _not_on_gpu()
     if ws is None:
         n = nvfp4_kv_attention_workspace_bytes(T, B, heads_q, heads, dim, max_q, max_len)
-        ws = torch.empty(max(n, ATTENTION_COUNTER_BYTES), dtype=torch.uint8, device=q.device)
-        ws[:ATTENTION_COUNTER_BYTES].zero_()
+        with _on(stream):
+            ws = torch.empty(max(n, ATTENTION_COUNTER_BYTES), dtype=torch.uint8, device=q.device)
+            ws[:ATTENTION_COUNTER_BYTES].zero_()
     _check("nvfp4_kv_attention",
            lib().nvfp4_kv_attention(q.data_ptr(), qs, T, B, heads_q, _ptr(q_offsets), max_q, cache.data_ptr(), pages,
                                     page_size, heads, dim, block_table.data_ptr(), table_stride if B > 1 else width, width,
