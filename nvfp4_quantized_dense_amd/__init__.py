@@ -422,6 +422,13 @@ def nvfp4_grouped_gemm(mode, a, a_scales, w_packed, N, K, alpha, masked_m=None, 
     return out
 
 
+def _scalar(t, name):
+    """The address of a global scale, which the kernels read as one fp32 number."""
+    if t.dtype != torch.float32 or t.numel() != 1:
+        raise ValueError(f"{name} must be one fp32 number")
+    return t.data_ptr()
+
+
 def _not_on_gpu():
     raise ValueError("all tensors must be on the GPU")
 
@@ -455,12 +462,13 @@ def _norm_outputs(x, w, residual, residual_out, codes, scales):
 def add_rmsnorm_nvfp4_quant(x, w, g_inv, residual=None, eps=1e-6, residual_out=None, codes=None, scales=None, stream=None):
     """z = x + residual, y = RMSnorm(z) * w, NVFP4(y) with g_inv: x [M, K] and residual bf16 or f32
     (residual None: z = x), w [K] -> (codes [M, K/2], scales [M, K/16], z). residual_out may be residual."""
+    g = _scalar(g_inv, "g_inv")
     M, K, rd, residual_out, codes, scales = _norm_outputs(x, w, residual, residual_out, codes, scales)
     if not g_inv.is_cuda:
         _not_on_gpu()
     _check("add_rmsnorm_nvfp4_quant",
            lib().add_rmsnorm_nvfp4_quant(x.data_ptr(), _dtype_code(x.dtype), _ptr(residual), rd, w.data_ptr(),
-                                         _dtype_code(w.dtype), eps, M, K, _ptr(g_inv), residual_out.data_ptr(),
+                                         _dtype_code(w.dtype), eps, M, K, g, residual_out.data_ptr(),
                                          codes.data_ptr(), scales.data_ptr(), _stream(stream)))
     return codes, scales, residual_out
 
@@ -491,11 +499,14 @@ def nvfp4_dequantize(codes, scales, g=None, row_g=None, out=None, out_dtype=torc
         out = torch.empty(M, K, dtype=out_dtype, device=codes.device)
     elif out.numel() != M * K or not out.is_contiguous():
         raise ValueError(f"out must be contiguous, [{M}, {K}]")
-    if scales.numel() * 16 != M * K:
-        raise ValueError(f"scales must be [{M}, {K // 16}]")
+    if codes.element_size() != 1 or scales.element_size() != 1 or scales.numel() * 16 != M * K:
+        raise ValueError(f"scales must be [{M}, {K // 16}], a byte each as codes")
+    g_at = None if g is None else _scalar(g, "g")
+    if row_g is not None and (row_g.dtype != torch.float32 or row_g.numel() != M or not row_g.is_contiguous()):
+        raise ValueError(f"row_g must be contiguous, fp32 [{M}]")
     if not (codes.is_cuda and scales.is_cuda and out.is_cuda and (g is None or g.is_cuda) and (row_g is None or row_g.is_cuda)):
         _not_on_gpu()
-    _check("nvfp4_dequantize", lib().nvfp4_dequantize(codes.data_ptr(), scales.data_ptr(), M, K, _ptr(g), _ptr(row_g),
+    _check("nvfp4_dequantize", lib().nvfp4_dequantize(codes.data_ptr(), scales.data_ptr(), M, K, g_at, _ptr(row_g),
                                                       out.data_ptr(), _dtype_code(out.dtype), _stream(stream)))
     return out
 
@@ -548,11 +559,12 @@ def nvfp4_kv_write(k, v, slots, k_g_inv, v_g_inv, cache, stream=None):
     Tv, vs = _token_rows(v, "v", heads, dim)
     if k.dtype != v.dtype or T != Tv or _list(slots, "slots", torch.int64).numel() != T:
         raise ValueError("k, v and slots must have one type and length")
+    kg, vg = _scalar(k_g_inv, "k_g_inv"), _scalar(v_g_inv, "v_g_inv")
     if not (k.is_cuda and v.is_cuda and slots.is_cuda and k_g_inv.is_cuda and v_g_inv.is_cuda and cache.is_cuda):
         _not_on_gpu()
     _check("nvfp4_kv_write",
            lib().nvfp4_kv_write(k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype), T, ks, vs, slots.data_ptr(),
-                                _ptr(k_g_inv), _ptr(v_g_inv), cache.data_ptr(), pages, page_size, heads, dim,
+                                kg, vg, cache.data_ptr(), pages, page_size, heads, dim,
                                 _stream(stream)))
     return cache
 
@@ -570,10 +582,11 @@ def nvfp4_kv_read(cache, slots, k_g, v_g, k=None, v=None, dtype=torch.bfloat16, 
         v = torch.empty_like(k)
     elif v.shape != shape or v.dtype != k.dtype or not v.is_contiguous():
         raise ValueError(f"v must be contiguous, {shape}, of k's type")
+    kg, vg = _scalar(k_g, "k_g"), _scalar(v_g, "v_g")
     if not (k.is_cuda and v.is_cuda and slots.is_cuda and k_g.is_cuda and v_g.is_cuda and cache.is_cuda):
         _not_on_gpu()
     _check("nvfp4_kv_read",
-           lib().nvfp4_kv_read(cache.data_ptr(), pages, page_size, heads, dim, slots.data_ptr(), T, _ptr(k_g), _ptr(v_g),
+           lib().nvfp4_kv_read(cache.data_ptr(), pages, page_size, heads, dim, slots.data_ptr(), T, kg, vg,
                                k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype), _stream(stream)))
     return k, v
 
@@ -625,6 +638,9 @@ def nvfp4_kv_attention(q, cache, block_table, seq_lens, k_g, v_g, q_offsets=None
             lse = torch.empty(T, heads_q, dtype=torch.float32, device=q.device)
     elif _list(lse, "lse", torch.float32).numel() != T * heads_q:
         raise ValueError("lse must be fp32 [tokens, heads_q]")
+    kg, vg = _scalar(k_g, "k_g"), _scalar(v_g, "v_g")
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
     if not (q.is_cuda and cache.is_cuda and block_table.is_cuda and seq_lens.is_cuda and k_g.is_cuda and v_g.is_cuda and
             out.is_cuda and (q_offsets is None or q_offsets.is_cuda) and (lse is None or lse.is_cuda) and
             (ws is None or ws.is_cuda)):
@@ -637,6 +653,6 @@ def nvfp4_kv_attention(q, cache, block_table, seq_lens, k_g, v_g, q_offsets=None
     _check("nvfp4_kv_attention",
            lib().nvfp4_kv_attention(q.data_ptr(), qs, T, B, heads_q, _ptr(q_offsets), max_q, cache.data_ptr(), pages,
                                     page_size, heads, dim, block_table.data_ptr(), table_stride if B > 1 else width, width,
-                                    seq_lens.data_ptr(), max_len, scale, window, _ptr(k_g), _ptr(v_g), ws.data_ptr(),
+                                    seq_lens.data_ptr(), max_len, scale, window, kg, vg, ws.data_ptr(),
                                     ws.nbytes, out.data_ptr(), _dtype_code(out.dtype), _ptr(lse), _stream(stream)))
     return out if lse is None else (out, lse)
