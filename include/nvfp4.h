@@ -500,7 +500,10 @@ int nvfp4_kv_read(const void* cache, int64_t pages, int64_t page_size, int64_t h
  * ws: nvfp4_kv_attention_workspace_bytes(...) bytes, 16-byte aligned. Its
  * first 4096 bytes (arrival counters of a split key axis) must be zero the
  * first time and are left zero by every call; calls of any sizes may share
- * it, one at a time.
+ * it, one at a time. The size is that of all calls of at most B sequences,
+ * max_q queries of each and max_len keys (heads_q, heads and head_dim the
+ * same), with any window: it is never less for larger sizes, so that a server
+ * asks once, for its largest. 0 for invalid arguments.
  */
 size_t nvfp4_kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t heads_q, int64_t heads, int64_t head_dim,
                                           int64_t max_q, int64_t max_len);

@@ -592,6 +592,7 @@ def nvfp4_kv_read(cache, slots, k_g, v_g, k=None, v=None, dtype=torch.bfloat16, 
 
 
 def nvfp4_kv_attention_workspace_bytes(T, B, heads_q, heads, head_dim, max_q, max_len) -> int:
+    """Bytes of ws for all attention calls of at most these sizes (never less for larger ones)."""
     return lib().nvfp4_kv_attention_workspace_bytes(T, B, heads_q, heads, head_dim, max_q, max_len)
 
 

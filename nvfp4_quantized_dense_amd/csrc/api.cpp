@@ -1150,9 +1150,8 @@ size_t nvfp4_kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t heads_q,
                                           int64_t max_q, int64_t max_len) {
   nvfp4::AttnPlan p;
   if (attn_sizes(T, B, heads_q, heads, head_dim, max_q, max_len, 0, p)) return 0;
-  size_t n = kAttnCounters * sizeof(uint32_t);
-  if (p.splits_bound > 1) n += align256((size_t)p.units * p.splits_bound * (size_t)p.part_floats * sizeof(float));
-  return n;
+  const int64_t floats = nvfp4::attn_workspace_floats(B, (int)heads_q, (int)heads, (int)head_dim, max_q, max_len);
+  return kAttnCounters * sizeof(uint32_t) + align256((size_t)floats * sizeof(float));
 }
 
 int nvfp4_kv_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64_t B, int64_t heads_q,

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "kv_attention_plan.h"
+
 namespace nvfp4 {
 
 // norm_quant.hip
@@ -64,24 +66,8 @@ struct AttnArgs {
   float* part;               // split partials
   uint32_t* counters;        // one per (row block, head, sequence), zero
 };
-// The split of a call, by its host-side sizes alone; units alone if there are
-// more than kAttnMaxUnits.
-constexpr int64_t kAttnMaxUnits = int64_t(1) << 23;
-struct AttnPlan {
-  bool tiled;           // kv_attention_tile.hip, else kv_attention.hip
-  int row_tiles;        // 16-row tiles per workgroup, tiled: per wave
-  int64_t units;        // row_blocks * B * heads
-  int rows;             // of a workgroup
-  int row_blocks;       // per (sequence, head)
-  int chunk;            // keys per split
-  int splits;           // most splits of one unit
-  int64_t splits_bound; // the same over all windows
-  int part_floats;      // per (unit, split)
-};
-AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t max_q, int64_t max_len, int64_t window);
 hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
 // kv_attention_tile.hip
 hipError_t launch_kv_attention_tile(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
-constexpr int attn_tile_max(int dim) { return dim == 64 ? 4 : 2; }  // most row tiles of a wave
 
 }  // namespace nvfp4
