@@ -47,11 +47,14 @@ class DecoderLayer:
         self.h_g_inv, self.alpha_d = 1.0 / self.h_g, self.h_g * self.g_d
         self.cache = nv.nvfp4_kv_cache(pages, page_size, heads, head_dim, device=device)
         self.ws = torch.zeros(nv.ATTENTION_COUNTER_BYTES, dtype=torch.uint8, device=device)
+        self.earlier = []
 
     def workspace(self, *sizes):
-        """One attention workspace for all calls, as large as the largest so far."""
+        """One attention workspace for all calls, as large as the largest so far. Those before it stay allocated: a
+        captured graph goes on using the address it was captured with."""
         need = nv.nvfp4_kv_attention_workspace_bytes(*sizes)
         if need > self.ws.numel():
+            self.earlier.append(self.ws)
             self.ws = torch.zeros(need, dtype=torch.uint8, device=self.ws.device)
         return self.ws
 

@@ -1,11 +1,18 @@
 """Calls on a stream of their own, given as an argument, while the current one
-goes on: the workspace they make for themselves is theirs until they are done."""
+goes on, and graphs: a workspace is a call's own until it is done, a graph's as
+long as it is replayed."""
+import os
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 import nvfp4_quantized_dense_amd as nv
 from test_gpu_kv_attention import KG, VG, Case, dev
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+from decoder_layer import Batch, DecoderLayer  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 BUSY = 20_000_000  # clock cycles, some milliseconds
@@ -74,3 +81,33 @@ def test_mlp_and_silu():
     assert int(want[0][0, 5:].max()) == 0 and int(want[1][0, 5:].max()) == 0 and int(want[0][0, :5].max()) > 0
     for got in beside(quant, M * I // 2):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_graph_captured_before_a_larger_call():
+    """The decoder layer example: a captured step replays on its own workspace after a larger call has made another."""
+    layer = DecoderLayer(256, 512, 8, 1, 64, pages=140, page_size=64, seed=5)
+    batch = Batch(layer, 2, 2100)
+    gen = torch.Generator("cuda").manual_seed(3)
+
+    def rows(n):
+        return torch.randn(n, 256, generator=gen, device="cuda").to(torch.bfloat16)
+
+    layer(rows(3000), rows(3000), **dict(batch.advance([2000, 1000]), max_len=2000))
+    x, r, call = rows(2), rows(2), batch.advance([1, 1])
+    layer.ws, layer.earlier = torch.zeros(nv.ATTENTION_COUNTER_BYTES, dtype=torch.uint8, device="cuda"), []
+    layer(x, r.clone(), **call)
+    small, start = layer.ws.numel(), r.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer(x, r, **call)
+    layer(rows(60), rows(60), **batch.advance([30, 30]))
+    assert layer.ws.numel() > small > nv.ATTENTION_COUNTER_BYTES
+    for _ in range(3):
+        junk = [torch.full((small,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        r.copy_(start)
+        graph.replay()
+        got = out.clone()
+        want = layer(x, start.clone(), **call)
+        torch.cuda.synchronize()
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+        del junk
