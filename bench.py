@@ -84,13 +84,13 @@ def algorithmic(M, H, I, mode, out_bytes):
 
 
 # Sources of the attention half, which no workload here runs.
-ATTENTION_SOURCES = ("attention.h", "norm_quant.hip", "kv_")
+ATTENTION_SOURCES = ("attention", "norm_quant.hip", "kv_")
 
 
 def kernel_source_hash() -> str:
-    """sha256[:16] over the MLP kernels' device sources, as recorded in profiles/*.md."""
+    """sha256[:16] over the MLP kernels' sources and their dispatch, as recorded in profiles/*.md."""
     h = hashlib.sha256()
-    for f in sorted(glob.glob(os.path.join(ROOT, "nvfp4_quantized_dense_amd", "csrc", "*.h*"))):
+    for f in sorted(glob.glob(os.path.join(ROOT, "nvfp4_quantized_dense_amd", "csrc", "*"))):
         if os.path.basename(f).startswith(ATTENTION_SOURCES):
             continue
         with open(f, "rb") as fh:

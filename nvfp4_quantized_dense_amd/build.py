@@ -14,8 +14,7 @@ OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnvfp4_mi355x.so")
 SOURCES = ["api.cpp", "quantize.hip", "repack.hip", "stream.hip", "stream_nt1.hip", "mid.hip", "gemv.hip", "fp4gemv.hip",
            "decode.hip", "decode16.hip", "tiled.hip", "tiled2.hip", "tiled16.hip", "silu_quant.hip", "prescale.hip",
-           "norm_quant.hip", "kv_cache.hip", "kv_attention.hip",
-           "kv_attention_tile.hip"]
+           "attention_api.cpp", "norm_quant.hip", "kv_cache.hip", "kv_attention.hip", "kv_attention_tile.hip"]
 # LLVM instruction-scheduling strategy per translation unit, where another
 # than the default measured faster on MI355X: the W4A16 tiled kernel with
 # max-ilp (forward at 256 / 4096 tokens, hidden 5120: 208 -> 198 us, 1948 ->
