@@ -55,25 +55,23 @@ __device__ __forceinline__ bool split_last(uint32_t* counter, int active, uint32
 // Joins the at most kJoinHere splits of a unit in split order, so that the
 // result does not depend on which workgroup arrived last. What this costs is
 // trips to device scope: partials are asked for together with the statistics.
-// (The loop over batches is run once; written without it the compiler unrolls
-// more, and one token of 64 sequences of up to 8192 keys takes 82 us, not 75.)
+// (Splits as a chain of branches: as a loop with a break one token of 64
+// sequences of up to 8192 keys took 78 us, not 68; without branches 69.)
 template <int D, int kRows>
 __device__ __forceinline__ void join_splits(const AttnArgs& a, const AttnPlan& p, const Seq& seq, unsigned unit, int active,
                                             int row0, int h, int G, float* lds) {
-  constexpr int kBatch = 16;
   const float vg = *a.v_g;
   const float* parts = a.part + (int64_t)unit * p.splits * p.part_floats;
   const Rsrc ra = make_rsrc(parts, (uint32_t)(active * p.part_floats * 4));
   const int live = (seq.rows - row0 < kRows ? seq.rows - row0 : kRows) * (D / 4);
-  f32x4 x[kBatch];
-  auto load = [&](int n, int s) {  // past the last split or row: zeros, unread
+  f32x4 x[kJoinHere];
+  auto load = [&](int n) {  // past the last split or row: zeros, unread
     const uint32_t at = (uint32_t)(8 * kRows + n * 16);
 #pragma unroll
-    for (int e = 0; e < kBatch; ++e)
-      x[e] = __builtin_bit_cast(f32x4, bload16_dev(ra, s + e < active && n < live ? at + (uint32_t)((s + e) * p.part_floats * 4)
-                                                                                  : kOutOfRange));
+    for (int s = 0; s < kJoinHere; ++s)
+      x[s] = __builtin_bit_cast(f32x4, bload16_dev(ra, s < active && n < live ? at + (uint32_t)(s * p.part_floats * 4) : kOutOfRange));
   };
-  load(threadIdx.x, 0);
+  load(threadIdx.x);
   float* jm = lds;  // [active][kRows] m, then l
   float* jl = lds + kJoinHere * kRows;
   for (int n = threadIdx.x; n < active * kRows; n += 256) {
@@ -88,16 +86,15 @@ __device__ __forceinline__ void join_splits(const AttnArgs& a, const AttnPlan& p
     for (int s = 0; s < active; ++s) m = __builtin_fmaxf(m, jm[s * kRows + rr]);
     float l = 0.0f;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < active; s += kBatch) {
-      if (s > 0 || n >= 256) load(n, s);
-#pragma unroll
-      for (int e = 0; e < kBatch; ++e) {
-        if (s + e >= active) break;
-        const float w = __builtin_amdgcn_exp2f(jm[(s + e) * kRows + rr] - m);
-        l += w * jl[(s + e) * kRows + rr];
-        v += x[e] * w;
+    if (n >= 256) load(n);
+    static_for<kJoinHere>([&](auto step) {
+      constexpr int s = decltype(step)::value;
+      if (s < active) {
+        const float w = __builtin_amdgcn_exp2f(jm[s * kRows + rr] - m);
+        l += w * jl[s * kRows + rr];
+        v += x[s] * w;
       }
-    }
+    });
     const int64_t orow = out_row(a, seq, row0 + rr, h, G);
     store4(a, orow * D + d, v * inverse_sum(l, vg));
     if (d == 0 && a.lse != nullptr) a.lse[orow] = lse_of(m, l);
