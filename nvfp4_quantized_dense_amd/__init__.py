@@ -134,7 +134,8 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
-_DTYPE_CODES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+_F32 = torch.float32
+_DTYPE_CODES = {torch.bfloat16: DTYPE_BF16, _F32: DTYPE_F32}
 
 
 def _dtype_code(dt):
@@ -424,7 +425,7 @@ def nvfp4_grouped_gemm(mode, a, a_scales, w_packed, N, K, alpha, masked_m=None, 
 
 def _scalar(t, name):
     """The address of a global scale, which the kernels read as one fp32 number."""
-    if t.dtype != torch.float32 or t.numel() != 1:
+    if t.dtype is not _F32 or t.numel() != 1:
         raise ValueError(f"{name} must be one fp32 number")
     return t.data_ptr()
 
@@ -502,7 +503,7 @@ def nvfp4_dequantize(codes, scales, g=None, row_g=None, out=None, out_dtype=torc
     if codes.element_size() != 1 or scales.element_size() != 1 or scales.numel() * 16 != M * K:
         raise ValueError(f"scales must be [{M}, {K // 16}], a byte each as codes")
     g_at = None if g is None else _scalar(g, "g")
-    if row_g is not None and (row_g.dtype != torch.float32 or row_g.numel() != M or not row_g.is_contiguous()):
+    if row_g is not None and (row_g.dtype is not _F32 or row_g.numel() != M or not row_g.is_contiguous()):
         raise ValueError(f"row_g must be contiguous, fp32 [{M}]")
     if not (codes.is_cuda and scales.is_cuda and out.is_cuda and (g is None or g.is_cuda) and (row_g is None or row_g.is_cuda)):
         _not_on_gpu()
@@ -525,7 +526,7 @@ def nvfp4_kv_cache(pages, page_size, heads, head_dim, device=None):
 def _cache_sizes(cache):
     """(pages, page_size, heads, head_dim) of a cache tensor."""
     shape = cache.shape
-    if len(shape) != 4 or cache.dtype != torch.uint8 or shape[3] % 18:
+    if len(shape) != 4 or cache.dtype is not torch.uint8 or shape[3] % 18:
         raise ValueError("cache must be uint8 [pages, heads, page_size / 16, 18 * head_dim]")
     if not cache.is_contiguous():
         raise ValueError("cache must be contiguous")
@@ -546,7 +547,7 @@ def _token_rows(t, name, heads, dim):
 
 def _list(t, name, dtype):
     """t, checked to be a dense tensor of dtype."""
-    if t.dtype != dtype or not t.is_contiguous():
+    if t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype}")
     return t
 
@@ -557,7 +558,7 @@ def nvfp4_kv_write(k, v, slots, k_g_inv, v_g_inv, cache, stream=None):
     pages, page_size, heads, dim = _cache_sizes(cache)
     T, ks = _token_rows(k, "k", heads, dim)
     Tv, vs = _token_rows(v, "v", heads, dim)
-    if k.dtype != v.dtype or T != Tv or _list(slots, "slots", torch.int64).numel() != T:
+    if k.dtype is not v.dtype or T != Tv or _list(slots, "slots", torch.int64).numel() != T:
         raise ValueError("k, v and slots must have one type and length")
     kg, vg = _scalar(k_g_inv, "k_g_inv"), _scalar(v_g_inv, "v_g_inv")
     if not (k.is_cuda and v.is_cuda and slots.is_cuda and k_g_inv.is_cuda and v_g_inv.is_cuda and cache.is_cuda):
@@ -580,7 +581,7 @@ def nvfp4_kv_read(cache, slots, k_g, v_g, k=None, v=None, dtype=torch.bfloat16, 
         raise ValueError(f"k must be contiguous, {shape}")
     if v is None:
         v = torch.empty_like(k)
-    elif v.shape != shape or v.dtype != k.dtype or not v.is_contiguous():
+    elif v.shape != shape or v.dtype is not k.dtype or not v.is_contiguous():
         raise ValueError(f"v must be contiguous, {shape}, of k's type")
     kg, vg = _scalar(k_g, "k_g"), _scalar(v_g, "v_g")
     if not (k.is_cuda and v.is_cuda and slots.is_cuda and k_g.is_cuda and v_g.is_cuda and cache.is_cuda):
@@ -610,13 +611,13 @@ def nvfp4_kv_attention(q, cache, block_table, seq_lens, k_g, v_g, q_offsets=None
     probabilities of 22 bits, bf16 with 11. Returns out (and lse)."""
     pages, page_size, heads, dim = _cache_sizes(cache)
     shape = q.shape
-    if len(shape) != 3 or q.dtype != torch.bfloat16:
+    if len(shape) != 3 or q.dtype is not torch.bfloat16:
         raise ValueError("q must be bf16 [tokens, heads_q, head_dim]")
     heads_q = shape[1]
     T, qs = _token_rows(q, "q", heads_q, dim)
     B = _list(seq_lens, "seq_lens", torch.int32).numel()
     table = block_table.shape
-    if len(table) != 2 or block_table.dtype != torch.int32 or table[0] != B:
+    if len(table) != 2 or block_table.dtype is not torch.int32 or table[0] != B:
         raise ValueError("block_table must be int32 [sequences, width]")
     width = table[1]
     table_stride, entry = block_table.stride()

@@ -9,8 +9,8 @@
 // splits are joined by the one that arrives last, more by a kernel of their own.
 //
 // Long axes are bound by memory: one token of 64 sequences of up to 8192 keys
-// (8 heads of 128, 308 MB) 72 us, 4.3 TB/s; of 4 of 131072 keys (604 MB) 117 us,
-// 5.2 TB/s. One sequence of 4097 keys takes 10.3 us, its chain of trips:
+// (8 heads of 128, 308 MB) 68 to 74 us, 4.2 to 4.5 TB/s; of 4 of 131072 keys
+// (604 MB) 118 us, 5.1 TB/s. One sequence of 4097 keys takes 10.3 us, its chain of trips:
 // lengths and page numbers, records, partials out, arrival, partials in. So
 // page numbers are asked for before the lengths, records before the query
 // rows, and a step's records while the step before is computed.

@@ -179,7 +179,7 @@ __device__ __forceinline__ uint32_t quad_transpose(uint32_t w, int k) {
   return k & 2 ? ((r >> 8) & 0x00FF00FFu) | (w & 0xFF00FF00u) : (w & 0x00FF00FFu) | ((r & 0x00FF00FFu) << 8);
 }
 
-// 8192 tokens of 8 heads of 128 (43 MB) take 10.9 us, bound by instruction
+// 8192 tokens of 8 heads of 128 (43 MB) take 10 to 12 us, bound by instruction
 // issue (two block scales with their exact divisions a lane) as much as by
 // memory; 64 tokens 3.8 us, the dependent trips: slots, rows, stores. Entries
 // of the list that fill an aligned quad of slots are written whole by the wave
@@ -276,7 +276,7 @@ __device__ __forceinline__ void store4_at(void* base, int64_t elem, const float*
 
 // Units as in k_kv_write: the four entries of a wave, neighbours in a record
 // as a rule, read the same V dwords. Bound by memory: 65536 tokens of 8 heads
-// of 128, 344 MB, in 53 us, 6.5 TB/s (most of it stores).
+// of 128, 344 MB, in 53 to 65 us, 5.3 to 6.5 TB/s (most of it stores).
 template <int D, bool F32>
 __global__ __launch_bounds__(256) void k_kv_read(CacheArgs c, const int64_t* slots, int64_t T, const float* kg,
                                                  const float* vg, void* k, void* v, Div groups) {

@@ -50,7 +50,7 @@ __device__ __forceinline__ void store8(void* p, int64_t c, const float (&v)[8]) 
 // the same for any split of the row over threads. The first CH chunks of 8
 // elements per thread stay in registers; a longer row (past 8192 elements) is
 // read a second time. Bound by memory: 8192 x 7168 in bf16 with a bf16
-// residual, 385 MB, in 64 us, 6 TB/s. One row is bound by its trips: load,
+// residual, 385 MB, in 59 to 68 us, 5.7 to 6.5 TB/s. One row is bound by its trips: load,
 // sum, 64-bit root, store.
 template <bool XF, bool RF, int NT, int CH>
 __global__ __launch_bounds__(NT) void k_add_rmsnorm_quant(NormArgs a) {
