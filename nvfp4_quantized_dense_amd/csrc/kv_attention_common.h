@@ -410,18 +410,19 @@ __device__ __forceinline__ void finish_rows(Rows<D, RT>& r) {
 #pragma unroll
   for (int t = 0; t < RT; ++t) r.l[t] = sum_xor32(sum_xor16(r.l[t]));
 }
-// The subtracted maximum of tile t's rows in units of log2, less kUp: what the
-// sum l and the outputs count from.
+// The subtracted maximum of tile t's rows, in units of log2.
 template <int D, int RT>
 __device__ __forceinline__ float row_maximum(const Rows<D, RT>& r, int t) {
-  return r.t[t] == kNoScore ? kNoKey : -r.a[t];
+  return r.t[t] == kNoScore ? kNoKey : kUp - r.a[t];
 }
 
 // ---- results ----------------------------------------------------------------
 
 __device__ __forceinline__ float inverse_sum(float l, float vg) { return l > 0.0f || l != l ? vg / l : 0.0f; }
+// l is 2^kUp as large: taken off before the logarithm, whose bits are then those
+// of the sum.
 __device__ __forceinline__ float lse_of(float m, float l) {
-  return l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
+  return l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l * __builtin_exp2f(-kUp))) * kLn2;
 }
 __device__ __forceinline__ void store4(const AttnArgs& a, int64_t at, const f32x4& r) {
   if (a.f32_out) {

@@ -99,3 +99,19 @@ def test_f32_output_has_more_than_11_bits(D, n, lens):
             ref = w @ v / w.sum()
             far = 2.0 ** -22 + 2.0 ** -24 * (16 * (np.abs(s).max() + abs(s.max())) + 16 + 2 * (L / 32 + 64))
             assert (np.abs(o[b * n + i, 0] - ref) <= far * ref + (2.0 ** -24 + L * 2.0 ** -32) * v.max()).all(), (b, i)
+
+
+@pytest.mark.parametrize("D,n", [(64, 1), (128, 1), (256, 1), (128, 70)])
+def test_lse_of_few_keys(D, n):
+    """One key's lse is its score (queries of one channel: a product); so are those of up to four keys, nearly: the scale's
+    and the exponent's roundings count a half step 2^-24 of the score each, exp2 and log2 a step 2^-23 of 1 each."""
+    lens = [1, 2, 3, 4] * 16 if n == 1 else [n]
+    c = Case(lens, [n] * len(lens), 1, 1, D, 16, seed=D)
+    c.q[:, :, :5] = 0
+    c.q[:, :, 6:] = 0
+    lse = c.run()[1].double().cpu().numpy()
+    for b, L in enumerate(lens):
+        for i in range(min(n, 4)):
+            s = c.k[b][:L - n + i + 1, 0, 5] * float(c.q[b * n + i, 0, 5]) * D ** -0.5
+            ref = s.max() + np.log(np.exp(s - s.max()).sum())
+            assert abs(lse[b * n + i, 0] - ref) <= 2.0 ** -22 + 2.0 ** -21 * np.abs(s).max(), (b, i)
