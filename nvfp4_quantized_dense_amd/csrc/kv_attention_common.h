@@ -253,11 +253,11 @@ __device__ __forceinline__ Stretch active_splits(const AttnArgs& a, const AttnPl
 
 // RT tiles of 16 rows: lane (quad, col) holds row col of a tile, of its output
 // channels 16 y + 4 quad + [0, 4). A raw score s has the probability
-// exp2(s f + a), 2^kUp times as large as under the subtracted maximum: kUp - a
-// is that, in units of log2. l: their sum
-// so far, over this lane's tokens; t: the raw score above which the maximum is
-// renewed, kNoScore before the first key. a is zero until then, so that a
-// hidden score of -inf gives the probability 0 whatever the query holds.
+// exp2(s f + a), 2^kUp times as large as it is under the subtracted maximum,
+// which is kUp - a in units of log2. l: their sum so far, over this lane's
+// tokens; t: the raw score above which the maximum is renewed, kNoScore before
+// the first key. a is zero until then, so that a hidden score of -inf gives the
+// probability 0 whatever the query holds.
 template <int D, int RT>
 struct Rows {
   f32x4 o[RT][D / 16];
