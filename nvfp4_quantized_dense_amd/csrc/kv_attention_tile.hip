@@ -16,8 +16,8 @@
 // at 64): 16 rows a wave more would spill, fewer share the making less (8 x
 // 1536 tokens x 64 heads over 8192 keys: RT 1 / 2 4215 / 2900 us, the latter
 // 1030 TFLOP/s; without the making and fetching, for the time alone, 1355).
-// Chunks of up to 2047 tokens of 3 sequences against up to 8192 keys: 440 to
-// 490 us, 825 to 920 TFLOP/s, the rest being unequal workgroups at the end.
+// Chunks of up to 2047 tokens of 3 sequences against up to 8192 keys: 418 to
+// 490 us, 825 to 965 TFLOP/s, the rest being unequal workgroups at the end.
 #include "kv_attention_common.h"
 
 namespace nvfp4 {
