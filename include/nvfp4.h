@@ -77,6 +77,13 @@ extern "C" {
 #define NVFP4_REPACK_SWIGLU 1 /* merged gate_up [2I, C], rows [gate; up] */
 
 /* Kernel-class override for tests and benchmarks (per calling thread). */
+#define NVFP4_ROPE_HALVES 0     /* channel i turns with i + rotary / 2 */
+#define NVFP4_ROPE_NEIGHBOURS 1 /* channel 2 i turns with 2 i + 1 */
+
+#define NVFP4_POOL_NO_PAGES 1 /* a pool's status: a request found too few free pages, */
+#define NVFP4_POOL_NO_TABLE 2 /* its length passed the block table's width, */
+#define NVFP4_POOL_NO_ROWS 4  /* its rows passed T */
+
 #define NVFP4_PATH_AUTO 0    /* choose by M */
 #define NVFP4_PATH_GEMV 1    /* decode GEMV sized for M <= 2: W4A4 on the FP4 matrix core with the
                                 blocks kept apart, W4A16 on the vector ALU (any M) */
@@ -513,6 +520,112 @@ int nvfp4_kv_attention(const uint16_t* q, int64_t q_stride, int64_t T, int64_t B
                        int64_t table_width, const int32_t* seq_lens, int64_t max_len, float scale, int64_t window,
                        const float* k_g, const float* v_g, void* ws, size_t ws_bytes, void* out, int out_dtype,
                        float* lse, void* stream);
+
+/*
+ * Pages and slots of a step, on the device. The pool holds the free pages of a
+ * cache (all layers that share one block table): int32 [4 + pages], number of
+ * free pages, status, two words for the library, then a stack of which the
+ * last free page is the next one taken. nvfp4_kv_pool_reset makes all `pages`
+ * pages (1 to 2^30 - 1) free, page 0 on top, and the status 0.
+ *
+ * nvfp4_kv_advance: counts[b] tokens (device int32 [B], B <= 65536) come to
+ * sequence b, or go from its end if negative (a finished request: its whole
+ * length or more; rejected drafts). seq_lens (device int32 [B]) and the first
+ * ceil(seq_lens[b] / page_size) entries of its row of block_table (device
+ * int32 [B, table_width]) say what it holds, before and after. Pages are
+ * taken from the pool in the order of the sequences; those given back lie on
+ * the stack as if the growth that took them had not been, and their entries
+ * become -1. For the tokens that come it writes, each where not NULL:
+ *   q_offsets  int32 [B + 1]  sums of the counts above 0, at most T
+ *   slots      int64 [T]      of row q_offsets[b] + i: where its key goes
+ *   positions  int32 [T]      seq_lens[b] before the call + i + position_offsets[b]
+ *                             (device int32 [B], or NULL)
+ * Rows of no sequence (a captured batch's padding) get slot -1, position 0. A
+ * request is refused as a whole if the pages that it and those before it ask
+ * for pass what was free before the call, its length the table's width or
+ * 2^30, or its last row T: its length and table stay, its rows get slot -1 and
+ * position 0, later requests are served if they can be, and the reason is OR-ed
+ * into the status, which nothing but a reset clears (the caller reads or
+ * clears it: the pool's second word). Pages given back in a call serve the
+ * next. One launch; calls on one pool must not overlap.
+ */
+size_t nvfp4_kv_pool_bytes(int64_t pages);
+int nvfp4_kv_pool_reset(void* pool, int64_t pages, void* stream);
+int nvfp4_kv_advance(const int32_t* counts, int64_t B, int32_t* seq_lens, int32_t* block_table, int64_t table_stride,
+                     int64_t table_width, int64_t page_size, void* pool, int64_t pages, int64_t T,
+                     const int32_t* position_offsets, int32_t* q_offsets, int64_t* slots, int32_t* positions, void* stream);
+
+/*
+ * Rotary positions. Of each head of x [T, heads, head_dim] (bf16 or f32, token
+ * stride in elements, whole 16-byte units, heads and channels dense; head_dim
+ * a multiple of 8, at most 1024) the first `rotary` channels (a multiple of
+ * 16, at most 512) turn in pairs, (i, i + rotary / 2) or (2 i, 2 i + 1) by
+ * `pairs`, the others are copied:
+ *   angle = positions[axis[i], t] * inv_freq[i] in 64 bits,
+ *   c = fl(factor * cos(angle)), s = fl(factor * sin(angle)) in fp32,
+ *   (x, y) -> (fl(fl(x c) - fl(y s)), fl(fl(y c) + fl(x s))), rounded to out_dtype.
+ * positions: device int32 [axes, T] (1 to 16 axes: time, height, width of a
+ * picture's tokens; axis stride in elements, 0 if all are alike); axis: device
+ * int32 [rotary / 2], the axis of each frequency (an axis outside the
+ * positions turns nothing), NULL: axis 0; inv_freq: device fp32 [rotary / 2].
+ * out may be x (one type and stride), not overlap it otherwise. With
+ * -inv_freq it is the inverse, and the gradient of the rotation.
+ */
+int nvfp4_rope(const void* x, int x_dtype, int64_t x_stride, int64_t T, int64_t heads, int64_t head_dim,
+               const int32_t* positions, int64_t axis_stride, int64_t axes, const float* inv_freq, const int32_t* axis,
+               int64_t rotary, int pairs, double factor, void* out, int out_dtype, int64_t out_stride, void* stream);
+
+/*
+ * nvfp4_rope of the queries to q_out, and nvfp4_kv_write of the turned keys
+ * and the values, in one launch. Keys are quantized from the turned fp32
+ * numbers, without a rounding in between: the same bits as nvfp4_rope to f32
+ * and nvfp4_kv_write. q [T, heads_q, head_dim], k, v of one type `dtype`;
+ * head_dim, slots and the cache as in nvfp4_kv_write; queries and keys of rows
+ * with a slot outside the cache are turned and skipped. heads_q may be 0.
+ */
+int nvfp4_rope_kv_write(const void* q, int64_t q_stride, int64_t heads_q, const void* k, const void* v, int dtype, int64_t T,
+                        int64_t k_stride, int64_t v_stride, const int32_t* positions, int64_t axis_stride, int64_t axes,
+                        const float* inv_freq, const int32_t* axis, int64_t rotary, int pairs, double factor,
+                        const int64_t* slots, const float* k_g_inv, const float* v_g_inv, void* cache, int64_t pages,
+                        int64_t page_size, int64_t heads, int64_t head_dim, void* q_out, int q_out_dtype, int64_t q_out_stride,
+                        void* stream);
+
+/*
+ * The mask rows of drafted trees from their parents: parents[t] (device int32
+ * [T]) is the number of row t's parent among its sequence's drafted tokens;
+ * one that is negative or not in front of the token itself stands for none.
+ * Sequences as in nvfp4_kv_attention (q_offsets or max_q each; max_q <= 4096,
+ * later rows of a sequence are not written). Bit d of row i's tree_words
+ * words: token d is i or an ancestor of it. positions (device int32 [T], or
+ * NULL): those of a sequence's rows become its first row's plus their depth
+ * (what nvfp4_kv_advance wrote for a chain becomes the tree's).
+ */
+int nvfp4_tree_mask(const int32_t* parents, int64_t T, int64_t B, const int32_t* q_offsets, int64_t max_q, uint64_t* tree,
+                    int64_t tree_words, int32_t* positions, void* stream);
+
+/*
+ * nvfp4_kv_attention with a window that keeps the first keys, and for drafted
+ * trees. With a window (window > 0) the keys 0 .. sinks - 1 stay visible to
+ * every query at or behind them: the query at p sees j <= p with j < sinks or
+ * j > p - window. Keys between the two stretches are not read, nor are the
+ * table's entries of pages that lie between them whole.
+ * tree (device, [T, tree_words], 8-byte aligned; NULL: causal): the n queries
+ * of a sequence are drafted tokens whose keys are its last n, n <= max_q <=
+ * 4096. Bit d % 64 of word d / 64 of a query's row says whether it sees the
+ * d-th drafted key (nvfp4_tree_mask makes rows from parents; a query sees
+ * itself only by its own bit, later tokens by theirs); of the keys in front
+ * of them it sees all or, with a window, those of its position, which is
+ * seq_lens[b] - n + (its bits - 1, at least 0). Bits from n or max_q on are
+ * ignored; if a sequence has more than max_q queries, keys of the ones past
+ * max_q are hidden. tree_words: ceil(max_q / 64) to 64. A window must be at
+ * least max_q, so that it hides no drafted key. Workspace as above.
+ */
+int nvfp4_kv_attention_masked(const uint16_t* q, int64_t q_stride, int64_t T, int64_t B, int64_t heads_q,
+                              const int32_t* q_offsets, int64_t max_q, const void* cache, int64_t pages, int64_t page_size,
+                              int64_t heads, int64_t head_dim, const int32_t* block_table, int64_t table_stride,
+                              int64_t table_width, const int32_t* seq_lens, int64_t max_len, float scale, int64_t window,
+                              int64_t sinks, const uint64_t* tree, int64_t tree_words, const float* k_g, const float* v_g,
+                              void* ws, size_t ws_bytes, void* out, int out_dtype, float* lse, void* stream);
 
 #ifdef __cplusplus
 }

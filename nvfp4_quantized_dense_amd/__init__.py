@@ -22,6 +22,8 @@ NVFP4_ERR_HIP = -3
 DTYPE_BF16, DTYPE_F32 = 0, 1
 MODE_W4A4, MODE_W4A16, MODE_W4A4_DYN, MODE_W4A16_AWQ = 0, 1, 2, 3
 REPACK_PLAIN, REPACK_SWIGLU = 0, 1
+ROPE_HALVES, ROPE_NEIGHBOURS = 0, 1
+POOL_NO_PAGES, POOL_NO_TABLE, POOL_NO_ROWS = 1, 2, 4
 PATH_AUTO, PATH_GEMV, PATH_STREAM, PATH_TILED, PATH_TILED64, PATH_MID = 0, 1, 2, 3, 4, 5
 
 _vp = ctypes.c_void_p
@@ -68,6 +70,15 @@ SIGNATURES = {
     "nvfp4_kv_attention_workspace_bytes": (_sz, [_i64] * 7),
     "nvfp4_kv_attention": (_int, [_vp, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp,
                                   _i64, _f32, _i64, _vp, _vp, _vp, _sz, _vp, _int, _vp, _vp]),
+    "nvfp4_kv_pool_bytes": (_sz, [_i64]),
+    "nvfp4_kv_pool_reset": (_int, [_vp, _i64, _vp]),
+    "nvfp4_kv_advance": (_int, [_vp, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "nvfp4_rope": (_int, [_vp, _int, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _int, _f64, _vp, _int, _i64, _vp]),
+    "nvfp4_rope_kv_write": (_int, [_vp, _i64, _i64, _vp, _vp, _int, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _int, _f64,
+                                   _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _int, _i64, _vp]),
+    "nvfp4_tree_mask": (_int, [_vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "nvfp4_kv_attention_masked": (_int, [_vp, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp,
+                                         _i64, _f32, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _sz, _vp, _int, _vp, _vp]),
     "mlp_forward_noalloc": (_int, [_int, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _vp]),
 }
 
@@ -592,6 +603,186 @@ def nvfp4_kv_read(cache, slots, k_g, v_g, k=None, v=None, dtype=torch.bfloat16, 
     return k, v
 
 
+def _same_gpu(*tensors):
+    """All of them (or None) on the current GPU, whose stream the call is on."""
+    here = torch._C._cuda_getDevice() if all(t is None or t.is_cuda for t in tensors) else _not_on_gpu()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"all tensors must be on the current GPU, cuda:{here}")
+
+
+POOL_HEAD = 4  # words of a pool before its stack
+
+
+def nvfp4_kv_pool_bytes(pages) -> int:
+    return int(lib().nvfp4_kv_pool_bytes(int(pages)))
+
+
+def _pool_pages(pool):
+    if _list(pool, "pool", torch.int32).dim() != 1 or pool.numel() <= POOL_HEAD:
+        raise ValueError(f"pool must be int32 [{POOL_HEAD} + pages]")
+    return pool.numel() - POOL_HEAD
+
+
+def nvfp4_kv_pool(pages, device="cuda", stream=None):
+    """The pool of a cache's pages, all of them free: int32 [4 + pages]; [0] counts the free ones, [1] is the status
+    (POOL_*: why requests were refused since it was last 0)."""
+    if nvfp4_kv_pool_bytes(pages) == 0:
+        raise ValueError(lib().nvfp4_last_error().decode())
+    with _on(stream):
+        pool = torch.empty(POOL_HEAD + pages, dtype=torch.int32, device=device)
+    return nvfp4_kv_pool_reset(pool, stream)
+
+
+def nvfp4_kv_pool_reset(pool, stream=None):
+    """All pages free again, page 0 the next. Returns the pool."""
+    pages = _pool_pages(pool)
+    _same_gpu(pool)
+    _check("nvfp4_kv_pool_reset", lib().nvfp4_kv_pool_reset(pool.data_ptr(), pages, _stream(stream)))
+    return pool
+
+
+def nvfp4_kv_advance(counts, seq_lens, block_table, pool, page_size, tokens, position_offsets=None, slots=None, positions=None,
+                     q_offsets=None, stream=None):
+    """counts int32 [B] tokens come to the sequences (or go, below 0): seq_lens int32 [B], block_table int32 [B, width] and
+    the pool are brought up to date, in place. Returns (slots int64 [tokens], positions int32 [tokens], q_offsets int32 [B + 1])
+    of the new tokens' rows; rows past them have slot -1. position_offsets int32 [B] is added to the positions."""
+    pages = _pool_pages(pool)
+    B = _list(counts, "counts", torch.int32).numel()
+    if _list(seq_lens, "seq_lens", torch.int32).numel() != B:
+        raise ValueError("counts and seq_lens must have one length")
+    table = block_table.shape
+    if len(table) != 2 or block_table.dtype is not torch.int32 or table[0] != B:
+        raise ValueError("block_table must be int32 [sequences, width]")
+    width = table[1]
+    table_stride, entry = block_table.stride()
+    if B and width > 1 and entry != 1:
+        raise ValueError("block_table must have dense rows")
+    if position_offsets is not None and _list(position_offsets, "position_offsets", torch.int32).numel() != B:
+        raise ValueError("position_offsets must have one element a sequence")
+    dev = counts.device
+    if slots is None:
+        slots = torch.empty(tokens, dtype=torch.int64, device=dev)
+    elif _list(slots, "slots", torch.int64).numel() != tokens:
+        raise ValueError(f"slots must be int64 [{tokens}]")
+    if positions is None:
+        positions = torch.empty(tokens, dtype=torch.int32, device=dev)
+    elif _list(positions, "positions", torch.int32).numel() != tokens:
+        raise ValueError(f"positions must be int32 [{tokens}]")
+    if q_offsets is None:
+        q_offsets = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    elif _list(q_offsets, "q_offsets", torch.int32).numel() != B + 1:
+        raise ValueError("q_offsets must have one more element than seq_lens")
+    _same_gpu(counts, seq_lens, block_table, pool, position_offsets, slots, positions, q_offsets)
+    _check("nvfp4_kv_advance",
+           lib().nvfp4_kv_advance(counts.data_ptr(), B, seq_lens.data_ptr(), block_table.data_ptr(),
+                                  table_stride if B > 1 else width, width, page_size, pool.data_ptr(), pages, tokens,
+                                  _ptr(position_offsets), q_offsets.data_ptr(), slots.data_ptr(), positions.data_ptr(),
+                                  _stream(stream)))
+    return slots, positions, q_offsets
+
+
+def nvfp4_rope_axes(sections, interleaved=False, device="cuda"):
+    """The axis of each frequency, int32 [sum(sections)]: sections[a] frequencies of axis a, in one run each or, interleaved,
+    the axes in turn until each has its share."""
+    left, axes = list(sections), []
+    if interleaved:
+        while any(left):
+            for a, n in enumerate(left):
+                if n:
+                    axes.append(a)
+                    left[a] -= 1
+    else:
+        for a, n in enumerate(left):
+            axes += [a] * n
+    return torch.tensor(axes, dtype=torch.int32, device=device)
+
+
+def _rope_plan(positions, inv_freq, axes, T, dim):
+    """(axis stride, axes, rotary channels) of a rotation of T tokens."""
+    n = _list(inv_freq, "inv_freq", _F32).numel()
+    if 2 * n > dim:
+        raise ValueError(f"inv_freq must have at most {dim // 2} elements")
+    if axes is not None and _list(axes, "axes", torch.int32).numel() != n:
+        raise ValueError("axes must have one element a frequency")
+    shape = positions.shape
+    if positions.dtype is not torch.int32 or len(shape) not in (1, 2) or shape[-1] != T or (T > 1 and positions.stride(-1) != 1):
+        raise ValueError(f"positions must be int32 [{T}] or [axes, {T}], each axis dense")
+    return (0, 1, 2 * n) if len(shape) == 1 else (positions.stride(0) if shape[0] > 1 else 0, shape[0], 2 * n)
+
+
+def nvfp4_rope(x, positions, inv_freq, axes=None, pairs=ROPE_HALVES, factor=1.0, out=None, out_dtype=None, stream=None):
+    """x [T, heads, head_dim] (bf16 or f32, token stride free) turned by its positions (int32 [T] or [axes, T]): frequency i of
+    inv_freq (fp32 [rotary / 2]) with the positions of axis axes[i] (int32 [rotary / 2]; None: the first), cosine and sine
+    times factor, channels paired by `pairs`. Returns out (x's type by default; may be x)."""
+    shape = x.shape
+    if len(shape) != 3:
+        raise ValueError("x must be [tokens, heads, head_dim]")
+    T, xs = _token_rows(x, "x", shape[1], shape[2])
+    step, count, rotary = _rope_plan(positions, inv_freq, axes, T, shape[2])
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
+    To, os_ = _token_rows(out, "out", shape[1], shape[2])
+    if To != T:
+        raise ValueError("out must have x's shape")
+    _same_gpu(x, positions, inv_freq, axes, out)
+    _check("nvfp4_rope",
+           lib().nvfp4_rope(x.data_ptr(), _dtype_code(x.dtype), xs, T, shape[1], shape[2], positions.data_ptr(), step, count,
+                            inv_freq.data_ptr(), _ptr(axes), rotary, pairs, factor, out.data_ptr(), _dtype_code(out.dtype), os_,
+                            _stream(stream)))
+    return out
+
+
+def nvfp4_rope_kv_write(q, k, v, positions, inv_freq, slots, k_g_inv, v_g_inv, cache, axes=None, pairs=ROPE_HALVES, factor=1.0,
+                        q_out=None, stream=None):
+    """nvfp4_rope of q [T, heads_q, head_dim] and k, and nvfp4_kv_write of the turned k and of v, in one launch; q, k and v of
+    one type. Returns the turned queries (bf16 unless q_out is given, which may be q)."""
+    pages, page_size, heads, dim = _cache_sizes(cache)
+    if len(q.shape) != 3:
+        raise ValueError("q must be [tokens, heads_q, head_dim]")
+    heads_q = q.shape[1]
+    T, qs = _token_rows(q, "q", heads_q, dim)
+    Tk, ks = _token_rows(k, "k", heads, dim)
+    Tv, vs = _token_rows(v, "v", heads, dim)
+    if q.dtype is not k.dtype or k.dtype is not v.dtype or T != Tk or T != Tv or _list(slots, "slots", torch.int64).numel() != T:
+        raise ValueError("q, k, v and slots must have one type and length")
+    step, count, rotary = _rope_plan(positions, inv_freq, axes, T, dim)
+    if q_out is None:
+        q_out = torch.empty(T, heads_q, dim, dtype=torch.bfloat16, device=q.device)
+    To, os_ = _token_rows(q_out, "q_out", heads_q, dim)
+    if To != T:
+        raise ValueError("q_out must have q's shape")
+    kg, vg = _scalar(k_g_inv, "k_g_inv"), _scalar(v_g_inv, "v_g_inv")
+    _same_gpu(q, k, v, positions, inv_freq, slots, k_g_inv, v_g_inv, cache, axes, q_out)
+    _check("nvfp4_rope_kv_write",
+           lib().nvfp4_rope_kv_write(q.data_ptr(), qs, heads_q, k.data_ptr(), v.data_ptr(), _dtype_code(q.dtype), T, ks, vs,
+                                     positions.data_ptr(), step, count, inv_freq.data_ptr(), _ptr(axes), rotary, pairs, factor,
+                                     slots.data_ptr(), kg, vg, cache.data_ptr(), pages, page_size, heads, dim, q_out.data_ptr(),
+                                     _dtype_code(q_out.dtype), os_, _stream(stream)))
+    return q_out
+
+
+def nvfp4_tree_mask(parents, q_offsets, max_q, positions=None, tree=None, stream=None):
+    """The masks of drafted trees for nvfp4_kv_attention: int64 [T, ceil(max_q / 64)], a bit for itself and each ancestor.
+    parents int32 [T]: the number of a token's parent in its sequence's draft (below 0: none); q_offsets int32 [B + 1] (None:
+    max_q tokens each). positions int32 [T] become the first row's of a sequence plus the depth, in place."""
+    T = _list(parents, "parents", torch.int32).numel()
+    if q_offsets is None:
+        B = T // max_q if max_q > 0 else 0
+    else:
+        B = _list(q_offsets, "q_offsets", torch.int32).numel() - 1
+    if tree is None:
+        tree = torch.empty(T, max(1, (max_q + 63) // 64), dtype=torch.int64, device=parents.device)
+    elif len(tree.shape) != 2 or _list(tree, "tree", torch.int64).shape[0] != T:
+        raise ValueError(f"tree must be int64 [{T}, words]")
+    if positions is not None and _list(positions, "positions", torch.int32).numel() != T:
+        raise ValueError(f"positions must be int32 [{T}]")
+    _same_gpu(parents, q_offsets, tree, positions)
+    _check("nvfp4_tree_mask", lib().nvfp4_tree_mask(parents.data_ptr(), T, B, _ptr(q_offsets), max_q, tree.data_ptr(),
+                                                    tree.shape[1], _ptr(positions), _stream(stream)))
+    return tree
+
+
 def nvfp4_kv_attention_workspace_bytes(T, B, heads_q, heads, head_dim, max_q, max_len) -> int:
     """Bytes of ws for all attention calls of at most these sizes (never less for larger ones)."""
     return lib().nvfp4_kv_attention_workspace_bytes(T, B, heads_q, heads, head_dim, max_q, max_len)
@@ -601,12 +792,16 @@ ATTENTION_COUNTER_BYTES = 4096
 
 
 def nvfp4_kv_attention(q, cache, block_table, seq_lens, k_g, v_g, q_offsets=None, max_q=None, max_len=None, scale=None,
-                       window=0, ws=None, out=None, out_dtype=torch.bfloat16, lse=None, return_lse=False, stream=None):
+                       window=0, ws=None, out=None, out_dtype=torch.bfloat16, lse=None, return_lse=False, stream=None, sinks=0,
+                       tree=None):
     """Causal attention of q bf16 [T, heads_q, head_dim] (token stride free) over the cache.
 
     block_table int32 [B, width], seq_lens int32 [B]; sequence b's queries are q[q_offsets[b]:q_offsets[b + 1]]
     (int32 [B + 1]; None: T / B each) at its last positions; rows of no sequence are not written. max_q, max_len:
-    bounds known on the host (default: T / B or T, and the table's width). scale: 1 / sqrt(head_dim) by default; window: visible keys of a query (0: all).
+    bounds known on the host (default: T / B or T, and the table's width). scale: 1 / sqrt(head_dim) by default; window: visible keys of a query (0: all),
+    sinks: first keys that stay visible behind it. tree int64 [T, words] (nvfp4_tree_mask): a sequence's queries are a drafted
+    tree, whose query sees the drafted keys of its bits and all keys in front of them (max_q at most 64 words, 4096, and at
+    most the window).
     ws: workspace whose first 4096 bytes are zero the first time; allocated if None. out_dtype fp32 computes with
     probabilities of 22 bits, bf16 with 11. Returns out (and lse)."""
     pages, page_size, heads, dim = _cache_sizes(cache)
@@ -640,6 +835,13 @@ def nvfp4_kv_attention(q, cache, block_table, seq_lens, k_g, v_g, q_offsets=None
             lse = torch.empty(T, heads_q, dtype=torch.float32, device=q.device)
     elif _list(lse, "lse", torch.float32).numel() != T * heads_q:
         raise ValueError("lse must be fp32 [tokens, heads_q]")
+    words = 0
+    if tree is not None:
+        if len(tree.shape) != 2 or _list(tree, "tree", torch.int64).shape[0] != T or tree.shape[1] < 1:
+            raise ValueError(f"tree must be int64 [{T}, words]")
+        words = tree.shape[1]
+        if not tree.is_cuda:
+            _not_on_gpu()
     kg, vg = _scalar(k_g, "k_g"), _scalar(v_g, "v_g")
     if ws is not None and not ws.is_contiguous():
         raise ValueError("ws must be contiguous")
@@ -652,6 +854,14 @@ def nvfp4_kv_attention(q, cache, block_table, seq_lens, k_g, v_g, q_offsets=None
         with _on(stream):
             ws = torch.empty(max(n, ATTENTION_COUNTER_BYTES), dtype=torch.uint8, device=q.device)
             ws[:ATTENTION_COUNTER_BYTES].zero_()
+    if sinks or tree is not None:
+        _check("nvfp4_kv_attention_masked",
+               lib().nvfp4_kv_attention_masked(q.data_ptr(), qs, T, B, heads_q, _ptr(q_offsets), max_q, cache.data_ptr(), pages,
+                                               page_size, heads, dim, block_table.data_ptr(), table_stride if B > 1 else width,
+                                               width, seq_lens.data_ptr(), max_len, scale, window, sinks, _ptr(tree), words, kg,
+                                               vg, ws.data_ptr(), ws.nbytes, out.data_ptr(), _dtype_code(out.dtype), _ptr(lse),
+                                               _stream(stream)))
+        return out if lse is None else (out, lse)
     _check("nvfp4_kv_attention",
            lib().nvfp4_kv_attention(q.data_ptr(), qs, T, B, heads_q, _ptr(q_offsets), max_q, cache.data_ptr(), pages,
                                     page_size, heads, dim, block_table.data_ptr(), table_stride if B > 1 else width, width,

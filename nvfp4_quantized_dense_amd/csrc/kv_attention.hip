@@ -106,8 +106,8 @@ __device__ __forceinline__ void join_splits(const AttnArgs& a, const AttnPlan& p
 template <int D, int RT>
 constexpr int kAttnWgs = D == 256 ? 3 - RT : RT == 2 ? 2 : D == 64 ? 4 : 3;
 
-// P: f16 parts of a probability.
-template <int D, int RT, int P>
+// P: f16 parts of a probability. MASKED: sinks or a tree mask.
+template <int D, int RT, int P, bool MASKED>
 __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArgs a, AttnPlan p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int kB = D / 16, kW = D / 32, kRows = 16 * RT;
@@ -126,15 +126,17 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
   const Seq seq = seq_of(a, b, G);
   if ((int64_t)rb * kRows >= seq.rows) return;
   const int row0 = (int)rb * kRows;
-  const Stretch all = active_splits(a, p, seq, row0, kRows, G);
-  const int hi_all = all.hi, lo_all = all.lo, active = all.splits;
-  const int hi_full = sees_hi(seq, row0 / G), lo_full = sees_lo(hi_all, a.window);  // [lo_full, hi_full) need no mask
+  const Stretch all = active_splits<MASKED>(a, p, seq, row0, kRows, G);
+  const int active = all.splits;
+  // [lo_full, hi_full) need no mask.
+  const int hi_full = MASKED && a.tree != nullptr ? tree_context(seq) : sees_hi(seq, row0 / G);
+  const int lo_full = sees_lo(all.hi, a.window);
   if (split >= active) return;
 
   // This wave's stretch, whole steps of 32 tokens. Its first records are asked
   // for before the query rows.
   const int s_first = all.start + split * p.chunk;
-  const int s_last = hi_all - s_first > p.chunk ? s_first + p.chunk : hi_all;
+  const int s_last = all.end - s_first > p.chunk ? s_first + p.chunk : all.end;
   const int steps = s_last > s_first ? (s_last - s_first + 31) / 32 : 0, per = (steps + 3) / 4;
   const int step0 = wave * per, step1 = step0 + per < steps ? step0 + per : steps;
 
@@ -143,7 +145,12 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
     VFrag<D> v[2];
     bool ok[2];
   };
+  int ahead = s_first + 32 * step0;  // the next step fetched
   auto fetch = [&](Pair& f) {
+    if constexpr (MASKED) {
+      if (ahead == all.head && all.gap > 0) walk.start((ahead + all.gap) >> 4);
+      ahead += 32;
+    }
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const Rsrc rec = walk.record(f.ok[x], lane);
@@ -154,13 +161,13 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
   };
   Pair fa, fb;
   if (step0 < step1) {
-    walk.start((s_first >> 4) + 2 * step0);
+    walk.start(all.key<MASKED>(ahead) >> 4);
     fetch(fa);
   }
   Rows<D, RT> r;
-  load_rows<D, RT>(r, a, seq, row0, h, G, quad, col);
+  load_rows<D, RT, MASKED>(r, a, seq, row0, h, G, quad, col);
   auto attend = [&](Pair& f, int base) {
-    const bool edge = base + 32 > hi_full || base < lo_full || !f.ok[0] || !f.ok[1];
+    const bool edge = needs_mask<MASKED>(a, base, lo_full, hi_full) || !f.ok[0] || !f.ok[1];
     f32x4 sc[RT][2];
 #pragma unroll
     for (int t = 0; t < RT; ++t) sc[t][0] = sc[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -176,11 +183,12 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
     }
     if (edge) {
       asm volatile("");  // a branch: most steps need no mask
-      hide_scores<D, RT>(r, sc, base, quad, f.ok);
+      if constexpr (MASKED) hide_masked<D, RT>(r, a, seq, sc, base, quad, f.ok);
+      else hide_scores<D, RT>(r, sc, base, quad, f.ok);
       // Tokens no row sees may never have been written: their V scales
       // become zero, so that no NaN code meets a zero probability.
 #pragma unroll
-      for (int x = 0; x < 2; ++x) f.v[x].s &= f.ok[x] ? byte_mask(base + 16 * x + 4 * quad, lo_all, hi_all) : 0u;
+      for (int x = 0; x < 2; ++x) f.v[x].s &= f.ok[x] ? seen_bytes<MASKED>(a, all, base + 16 * x + 4 * quad) : 0u;
     }
     f16x8 pf[P][RT];
     float mx[RT];
@@ -195,10 +203,10 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
     for (int st = step0; st < step1; st += 2) {
       const int base = s_first + 32 * st;
       if (st + 1 < step1) fetch(fb);
-      attend(fa, base);
+      attend(fa, all.key<MASKED>(base));
       if (st + 1 >= step1) break;
       if (st + 2 < step1) fetch(fa);
-      attend(fb, base + 32);
+      attend(fb, all.key<MASKED>(base + 32));
     }
   }
   finish_rows<D, RT>(r);
@@ -261,7 +269,7 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
 // the order of the runs, whatever the timing. In one workgroup a unit (the
 // last to arrive) it took 64 rows 5 us a split; so, spread over the chip and
 // with 8 loads in flight a thread, about 5 us in all.
-template <int D>
+template <int D, bool MASKED>
 __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, AttnPlan p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int kSlices = 4, kRun = 8, kThreads = D / 4, kRowsHere = 256 / kThreads / kSlices;
@@ -274,7 +282,7 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, AttnPlan p) {
   const int rr = blockIdx.y * kRowsHere + slot / kSlices;
   if ((int64_t)rb * rows_wg + blockIdx.y * kRowsHere >= seq.rows) return;
   const int row0 = (int)rb * rows_wg;
-  const int active = active_splits(a, p, seq, row0, rows_wg, G).splits;
+  const int active = active_splits<MASKED>(a, p, seq, row0, rows_wg, G).splits;
   if (active == 1) return;
   const float* part = a.part + (int64_t)unit * p.splits * p.part_floats;
   float m = kNoKey, l = 0.0f;
@@ -330,23 +338,82 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, AttnPlan p) {
 #endif
 }
 
-template <int D, int P>
+// The rows of a drafted tree's mask from its parents, a thread a row: it walks
+// up its ancestors, whose numbers only fall, so that the words are finished
+// from the last to the first. A chain of LDS reads as long as the row is deep.
+constexpr int kTreeThreads = 256;
+__global__ __launch_bounds__(kTreeThreads) void k_tree_mask(TreeArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ int parent[kMaxTree];
+  const int64_t b = blockIdx.x;
+  int64_t q0 = b * a.max_q, n = a.max_q;
+  if (a.q_offsets != nullptr) {
+    q0 = a.q_offsets[b];
+    n = a.q_offsets[b + 1] - q0;
+    if (q0 < 0 || q0 > a.T) n = 0;
+    if (n > a.T - q0) n = a.T - q0;
+    if (n > a.max_q) n = a.max_q;
+  }
+  const int row0 = (int)blockIdx.y * kTreeThreads, i = row0 + (int)threadIdx.x;
+  if (row0 >= n) return;
+  const int first = a.positions != nullptr ? a.positions[q0] : 0;
+  for (int at = threadIdx.x; at < row0 + kTreeThreads && at < n; at += kTreeThreads) {
+    const int p = a.parents[q0 + at];
+    parent[at] = p < at ? p : -1;
+  }
+  __syncthreads();
+  if (i >= n) return;
+  uint64_t* out = a.tree + (q0 + i) * a.tree_words;
+  int word = a.tree_words - 1, depth = -1;
+  uint64_t bits = 0;
+  for (int at = i; at >= 0; at = parent[at]) {
+    for (; word > at >> 6; --word) {
+      out[word] = bits;
+      bits = 0;
+    }
+    bits |= uint64_t(1) << (at & 63);
+    ++depth;
+  }
+  for (; word >= 0; --word) {
+    out[word] = bits;
+    bits = 0;
+  }
+  // The first row's depth is 0: its position, which the others read, stays.
+  if (a.positions != nullptr && i > 0) a.positions[q0 + i] = first + depth;
+#endif
+}
+
+template <int D, int P, bool MASKED>
 void launch_parts(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
   const dim3 grid((unsigned)p.units, (unsigned)p.splits);
-  if (p.row_tiles == 1) k_kv_attention<D, 1, P><<<grid, dim3(256), 0, s>>>(a, p);
-  else k_kv_attention<D, 2, P><<<grid, dim3(256), 0, s>>>(a, p);
+  if (p.row_tiles == 1) k_kv_attention<D, 1, P, MASKED><<<grid, dim3(256), 0, s>>>(a, p);
+  else k_kv_attention<D, 2, P, MASKED><<<grid, dim3(256), 0, s>>>(a, p);
 }
 template <int D>
 void launch_stream(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
-  if (a.f32_out) launch_parts<D, 2>(a, p, s);
-  else launch_parts<D, 1>(a, p, s);
+  if (attn_masked(a)) {
+    if (a.f32_out) launch_parts<D, 2, true>(a, p, s);
+    else launch_parts<D, 1, true>(a, p, s);
+  } else if (a.f32_out) {
+    launch_parts<D, 2, false>(a, p, s);
+  } else {
+    launch_parts<D, 1, false>(a, p, s);
+  }
 }
 template <int D>
 void launch_join(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
-  k_kv_join<D><<<dim3((unsigned)p.units, (unsigned)(p.rows * D / 256)), dim3(256), 0, s>>>(a, p);
+  const dim3 grid((unsigned)p.units, (unsigned)(p.rows * D / 256));
+  if (attn_masked(a)) k_kv_join<D, true><<<grid, dim3(256), 0, s>>>(a, p);
+  else k_kv_join<D, false><<<grid, dim3(256), 0, s>>>(a, p);
 }
 
 }  // namespace
+
+hipError_t launch_tree_mask(const TreeArgs& a, int64_t B, hipStream_t s) {
+  const dim3 grid((unsigned)B, (unsigned)((a.max_q + kTreeThreads - 1) / kTreeThreads));
+  k_tree_mask<<<grid, dim3(kTreeThreads), 0, s>>>(a);
+  return hipGetLastError();
+}
 
 hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
   if (p.tiled) {

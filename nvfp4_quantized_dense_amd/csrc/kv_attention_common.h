@@ -236,19 +236,72 @@ __device__ __forceinline__ int sees_lo(int hi, int64_t window) {
   return window > 0 && hi > window ? (int)(hi - window) : 0;
 }
 
-// The keys [lo, hi) that any of a workgroup's rows sees (rows row0 on, row0
-// one of them), walked over from `start` on in `splits` stretches.
+// Keys in front of the drafted ones, and where the drafted ones that a tree
+// mask speaks of end: a call computes at most max_q of a sequence's queries.
+__device__ __forceinline__ int tree_context(const Seq& s) {
+  const int64_t c = (int64_t)s.len - s.nq;
+  return (int)(c < 0 ? 0 : c);
+}
+__device__ __forceinline__ int tree_hi(const AttnArgs& a, const Seq& s) {
+  return sees_hi(s, (int)(s.nq < a.max_q ? s.nq : a.max_q) - 1);
+}
+
+// The keys that any of a workgroup's rows (row0 on, row0 one of them) sees:
+// [lo, hi) and, MASKED, the sinks. They are walked over as one axis from
+// `start` to `end` in `splits` stretches, whole steps of 32: its places up to
+// `head` are the keys of that number, later ones lie `gap` keys further on.
 struct Stretch {
-  int lo, hi, start, splits;
+  int lo, hi, start, end, splits, head, gap;
+  template <bool MASKED>
+  __device__ __forceinline__ int key(int at) const {
+    if constexpr (MASKED) return at < head ? at : at + gap;
+    return at;
+  }
 };
+template <bool MASKED>
 __device__ __forceinline__ Stretch active_splits(const AttnArgs& a, const AttnPlan& p, const Seq& seq, int row0, int rows, int G) {
   const int last = seq.rows - 1 < row0 + rows - 1 ? seq.rows - 1 : row0 + rows - 1;
   Stretch s;
-  s.hi = sees_hi(seq, last / G);
-  s.lo = sees_lo(sees_hi(seq, row0 / G), a.window);
-  s.start = s.lo & ~31;
-  s.splits = s.hi > s.lo ? (s.hi - s.start + p.chunk - 1) / p.chunk : 1;
+  s.head = s.gap = 0;
+  if constexpr (MASKED) {
+    const bool tree = a.tree != nullptr;
+    s.hi = tree ? tree_hi(a, seq) : sees_hi(seq, last / G);
+    s.lo = sees_lo(sees_hi(seq, tree ? 0 : row0 / G), a.window);
+    const int from = s.lo & ~31;
+    s.head = a.sinks < from ? ((int)a.sinks + 31) & ~31 : from;
+    s.gap = from - s.head;
+    s.start = 0;
+    s.end = s.hi - s.gap;
+    s.splits = s.end > 0 ? (s.end + p.chunk - 1) / p.chunk : 1;
+  } else {
+    s.hi = sees_hi(seq, last / G);
+    s.lo = sees_lo(sees_hi(seq, row0 / G), a.window);
+    s.start = s.lo & ~31;
+    s.end = s.hi;
+    s.splits = s.hi > s.lo ? (s.hi - s.start + p.chunk - 1) / p.chunk : 1;
+  }
   return s;
+}
+
+// Bits 0 .. n - 1.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u;
+}
+// Of row `row`'s mask: which of the drafted keys d .. d + 31 it sees; keys in
+// front of the first (d < 0) count as seen, past the mask's words as hidden.
+__device__ __forceinline__ uint32_t tree_bits(const AttnArgs& a, int row, int d) {
+  if (d <= -32) return ~0u;
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(a.tree + (int64_t)row * a.tree_words);
+  const int n = 2 * a.tree_words, i = d >> 5;
+  const uint32_t lo = i < 0 ? ~0u : i < n ? w[i] : 0u, hi = i + 1 < n ? w[i + 1] : 0u;
+  return __builtin_amdgcn_alignbit(hi, lo, (uint32_t)d & 31u);
+}
+// How many of its n first drafted keys it sees.
+__device__ __forceinline__ int tree_count(const AttnArgs& a, int row, int n) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(a.tree + (int64_t)row * a.tree_words);
+  int c = 0;
+  for (int i = 0; i < 2 * a.tree_words && 32 * i < n; ++i) c += __builtin_popcount(w[i] & low_bits(n - 32 * i));
+  return c;
 }
 
 // RT tiles of 16 rows: lane (quad, col) holds row col of a tile, of its output
@@ -263,10 +316,11 @@ struct Rows {
   f32x4 o[RT][D / 16];
   f16x8 q[RT][D / 32];
   float a[RT], l[RT], f[RT], t[RT];
-  int lo[RT], n[RT];  // keys seen: lo .. lo + n - 1
+  int lo[RT], n[RT];  // keys seen: lo .. lo + n - 1, but for what sinks and a tree change
+  int row[RT];        // MASKED: in the tree mask
 };
 
-template <int D, int RT>
+template <int D, int RT, bool MASKED>
 __device__ __forceinline__ void load_rows(Rows<D, RT>& r, const AttnArgs& a, const Seq& seq, int row0, int h, int G,
                                           int quad, int col) {
   constexpr int kW = D / 32;
@@ -276,8 +330,20 @@ __device__ __forceinline__ void load_rows(Rows<D, RT>& r, const AttnArgs& a, con
     const int row = row0 + 16 * t + col;
     const bool live = row < seq.rows;
     const int i = live ? (int)((unsigned)row / (unsigned)G) : 0;
-    const int head = h * G + row - i * G, hi = live ? sees_hi(seq, i) : 0;
+    const int head = h * G + row - i * G;
+    int hi = live ? sees_hi(seq, i) : 0;
     r.lo[t] = sees_lo(hi, a.window);
+    if constexpr (MASKED) {
+      r.row[t] = (int)seq.q0 + i;
+      if (live && a.tree != nullptr) {
+        // A query's position is by its depth, the drafted keys it sees but itself.
+        hi = tree_hi(a, seq);
+        if (a.window > 0) {
+          const int depth = tree_count(a, r.row[t], (int)(seq.nq < a.max_q ? seq.nq : a.max_q)) - 1;
+          r.lo[t] = sees_lo(sees_hi(seq, depth < 0 ? 0 : depth), a.window);
+        }
+      }
+    }
     r.n[t] = hi - r.lo[t];
     r.t[t] = kNoScore;
     r.a[t] = r.l[t] = 0.0f;
@@ -342,6 +408,38 @@ __device__ __forceinline__ void hide_scores(const Rows<D, RT>& r, f32x4 (&sc)[RT
         sc[t][x][e] = (unsigned)(at + 16 * x + e) < (unsigned)n ? sc[t][x][e] : -__builtin_inff();
     }
   }
+}
+
+// The same where sinks or a tree decide, a bit a key.
+template <int D, int RT>
+__device__ __forceinline__ void hide_masked(const Rows<D, RT>& r, const AttnArgs& a, const Seq& seq, f32x4 (&sc)[RT][2], int base,
+                                            int quad, const bool (&ok)[2]) {
+  const uint32_t sinks = low_bits((int)a.sinks - base), pages = (ok[0] ? 0xFFFFu : 0u) | (ok[1] ? 0xFFFF0000u : 0u);
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    uint32_t see = low_bits(r.lo[t] + r.n[t] - base) & (~low_bits(r.lo[t] - base) | sinks) & pages;
+    if (a.tree != nullptr && see != 0) see &= tree_bits(a, r.row[t], base - (int)((int64_t)seq.len - seq.nq));
+    see >>= 4 * quad;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[t][x][e] = see & (1u << (16 * x + e)) ? sc[t][x][e] : -__builtin_inff();
+  }
+}
+
+// Whether a wave's step of 32 keys needs the mask: [lo_full, hi_full) and the
+// sinks are seen by all its rows.
+template <bool MASKED>
+__device__ __forceinline__ bool needs_mask(const AttnArgs& a, int base, int lo_full, int hi_full) {
+  if constexpr (MASKED) return base + 32 > hi_full || (base < lo_full && base + 32 > a.sinks);
+  return base + 32 > hi_full || base < lo_full;
+}
+// Keeps the bytes of those of a quad's tokens that some row of the workgroup sees.
+template <bool MASKED>
+__device__ __forceinline__ uint32_t seen_bytes(const AttnArgs& a, const Stretch& s, int first) {
+  uint32_t m = byte_mask(first, s.lo, s.hi);
+  if constexpr (MASKED) m |= byte_mask(first, 0, a.sinks < s.hi ? (int)a.sinks : s.hi);
+  return m;
 }
 
 template <int RT>

@@ -28,7 +28,8 @@ constexpr int attn_tile_max(int dim) { return dim == 64 ? 4 : 2; }  // most row 
 constexpr int64_t attn_tile_slots(int dim) { return dim == 256 ? 256 : 512; }
 constexpr int64_t kAttnSlots = 1024, kAttnTileKeys = 256, kAttnKeys = 512, kAttnMaxSplits = 256;
 
-inline AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t max_q, int64_t max_len, int64_t window) {
+inline AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t max_q, int64_t max_len, int64_t window,
+                          int64_t sinks = 0, bool tree = false) {
   AttnPlan p{};
   const int64_t G = heads_q / heads, rows = max_q * G;
   int64_t per, slots;  // rows of a workgroup, workgroups that fill the chip
@@ -40,7 +41,7 @@ inline AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t ma
     // Few workgroups: smaller ones, unless their rows pay for the keys' second
     // making (8 heads, group 8: 16 x 16000 keys 28.2 us with 64 rows, 32.4 with
     // 128; 128 tokens x 8192 keys 66 and 58 us).
-    const int64_t keys = window > 0 && window + 64 < max_len ? window + 64 : max_len;
+    const int64_t keys = window > 0 && window + 64 + sinks < max_len ? window + 64 + sinks : max_len;
     if (blocks * B * heads < slots && (keys <= 2048 || rows <= 512)) blocks = (rows + 63) / 64;
     p.row_tiles = (int)((rows + 64 * blocks - 1) / (64 * blocks));
     per = 64 * p.row_tiles;
@@ -59,13 +60,15 @@ inline AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t ma
   p.rows = (int)per;
   p.part_floats = (int)per * (dim + 2);
   // Keys that a unit reads at most, from a multiple of 32 on: its rows are of
-  // at most (per - 1) / G + 2 queries. (With a window the more splits for all
+  // at most (per - 1) / G + 2 queries, or all see a tree's last key, and the
+  // sinks are walked in front of it. (With a window the more splits for all
   // max_q queries' keys are mostly empty: 1000 tokens of 2 sequences, 20 heads
   // on 4, window 128 take 24 us so, 51 with those.)
   int64_t span = max_len;
   int64_t queries = (per - 1) / G + 2;
-  if (queries > max_q) queries = max_q;
-  if (window > 0 && window + queries + 30 < span) span = window + queries + 30;
+  if (queries > max_q || tree) queries = max_q;
+  const int64_t head = (sinks + 31) / 32 * 32;
+  if (window > 0 && head + window + queries + 30 < span) span = head + window + queries + 30;
   span = (span + 31) / 32 * 32;
   // At least 512 keys a split: one token of 4 sequences of 8000 keys 15.4 us
   // so, 21.1 with 256 (16 heads of 128 a kv head). Tiled 256, as a workgroup
@@ -107,7 +110,7 @@ inline AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t ma
 }
 
 // Floats of the partials of any call of at most B sequences, max_q queries of
-// each and max_len keys, with any window: at least units * splits * part_floats
+// each and max_len keys, with any window, sinks and trees: at least units * splits * part_floats
 // of all their plans that split, and itself never less for larger sizes.
 //   Few rows: splits <= slots / units rounded up, slots <= kAttnSlots, so
 //   units * splits < units + kAttnSlots, and units < kAttnSlots or splits = 1.

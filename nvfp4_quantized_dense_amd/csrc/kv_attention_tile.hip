@@ -28,8 +28,8 @@ constexpr int kTile = 64;  // keys
 
 #endif
 
-// P: f16 parts of a probability.
-template <int D, int RT, int P>
+// P: f16 parts of a probability. MASKED: sinks or a tree mask.
+template <int D, int RT, int P, bool MASKED>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(AttnArgs a, AttnPlan p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int kB = D / 16, kW = D / 32, kRows = 64 * RT;
@@ -53,21 +53,24 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
   const Seq seq = seq_of(a, b, G);
   if ((int64_t)rb * kRows >= seq.rows) return;
   const int row0 = (int)rb * kRows;
-  const Stretch all = active_splits(a, p, seq, row0, kRows, G);
-  const int hi_all = all.hi, lo_all = all.lo, active = all.splits;
+  const Stretch all = active_splits<MASKED>(a, p, seq, row0, kRows, G);
+  const int active = all.splits;
   if (split >= active) return;
   const int s_first = all.start + split * p.chunk;
-  const int s_last = hi_all - s_first > p.chunk ? s_first + p.chunk : hi_all;
+  const int s_last = all.end - s_first > p.chunk ? s_first + p.chunk : all.end;
   const int tiles = s_last > s_first ? (s_last - s_first + kTile - 1) / kTile : 0;
 
   Rows<D, RT> r;
   const int wrow0 = row0 + wave * 16 * RT;
-  load_rows<D, RT>(r, a, seq, wrow0, h, G, quad, col);
+  load_rows<D, RT, MASKED>(r, a, seq, wrow0, h, G, quad, col);
   // Keys that all of this wave's rows see, [lo_full, hi_full), need no mask.
   int hi_full = 0, lo_full = 0;
   if (wrow0 < seq.rows) {
     hi_full = sees_hi(seq, wrow0 / G);
-    lo_full = sees_lo(sees_hi(seq, (seq.rows < wrow0 + 16 * RT ? seq.rows - 1 : wrow0 + 16 * RT - 1) / G), a.window);
+    if (MASKED && a.tree != nullptr) {
+      hi_full = tree_context(seq);
+      lo_full = sees_lo(all.hi, a.window);
+    } else lo_full = sees_lo(sees_hi(seq, (seq.rows < wrow0 + 16 * RT ? seq.rows - 1 : wrow0 + 16 * RT - 1) / G), a.window);
   }
 
   // Wave w brings K of the tile's record w and half w & 1 of V's channels of
@@ -78,12 +81,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
   bool ok[2] = {true, true};
   // Before what was fetched becomes operands: tokens no row sees may never
   // have been written. Their V scales become zero, so that no NaN code meets
-  // a zero probability. `base`: the tile's first key.
+  // a zero probability. `base`: the tile's first place.
   auto clear_v = [&](int base) {
-    base += 32 * pair;
-    if (base < lo_all || base + 32 > hi_all || !ok[0] || !ok[1]) {
+    base = all.key<MASKED>(base + 32 * pair);
+    if (needs_mask<MASKED>(a, base, all.lo, all.hi) || !ok[0] || !ok[1]) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) fv[x].s &= ok[x] ? byte_mask(base + 16 * x + 4 * quad, lo_all, hi_all) : 0u;
+      for (int x = 0; x < 2; ++x) fv[x].s &= ok[x] ? seen_bytes<MASKED>(a, all, base + 16 * x + 4 * quad) : 0u;
     }
   };
   // Operand n of the kB that this wave makes of what it fetched: K and V in
@@ -153,10 +156,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
     for (int t = 0; t < RT; ++t) asm volatile("" : "+v"(mx[t]), "+v"(r.l[t]));  // computed in here
   };
   auto renew = [&](f32x4 (&sc)[RT][2], float (&mx)[RT], int at, uint32_t oks) {
-    if (at + 32 > hi_full || at < lo_full || oks != 0x101u) {
+    at = all.key<MASKED>(at);
+    if (needs_mask<MASKED>(a, at, lo_full, hi_full) || oks != 0x101u) {
       asm volatile("");  // a branch: most pairs need no mask
       const bool okx[2] = {(oks & 255u) != 0, oks >> 8 != 0};
-      hide_scores<D, RT>(r, sc, at, quad, okx);
+      if constexpr (MASKED) hide_masked<D, RT>(r, a, seq, sc, at, quad, okx);
+      else hide_scores<D, RT>(r, sc, at, quad, okx);
       lane_maximum<RT>(sc, mx);
     }
     renew_maximum<D, RT>(r, mx);
@@ -168,8 +173,17 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
   };
   if (tiles > 0) {
     Walk<D> walk(a, b, h, s_first >> 4, lane);
-    walk.start((s_first >> 4) + 2 * pair);
+    int ahead = s_first + 32 * pair;  // the next of this wave's pairs fetched
+    walk.start(all.key<MASKED>(ahead) >> 4);
+    bool jump = ahead < all.head;
     auto fetch = [&] {
+      if constexpr (MASKED) {
+        if (jump && ahead >= all.head) {
+          walk.start((ahead + all.gap) >> 4);
+          jump = false;
+        }
+        ahead += kTile;
+      }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const Rsrc rec = walk.record(ok[x], lane);
@@ -250,8 +264,14 @@ void launch_rt(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
   if constexpr (RT <= attn_tile_max(D)) {
     if (p.row_tiles != RT) return launch_rt<D, RT + 1>(a, p, s);
     const dim3 grid((unsigned)p.units, (unsigned)p.splits);
-    if (a.f32_out) k_kv_attention_tile<D, RT, 2><<<grid, dim3(256), 0, s>>>(a, p);
-    else k_kv_attention_tile<D, RT, 1><<<grid, dim3(256), 0, s>>>(a, p);
+    if (attn_masked(a)) {
+      if (a.f32_out) k_kv_attention_tile<D, RT, 2, true><<<grid, dim3(256), 0, s>>>(a, p);
+      else k_kv_attention_tile<D, RT, 1, true><<<grid, dim3(256), 0, s>>>(a, p);
+    } else if (a.f32_out) {
+      k_kv_attention_tile<D, RT, 2, false><<<grid, dim3(256), 0, s>>>(a, p);
+    } else {
+      k_kv_attention_tile<D, RT, 1, false><<<grid, dim3(256), 0, s>>>(a, p);
+    }
   }
 }
 

@@ -1,5 +1,8 @@
 // kv_cache.hip -- keys and values into the paged NVFP4 cache as they are
-// written, and back to dense rows.
+// written, turned by their positions where the caller wants that, and back to
+// dense rows; and which pages and slots a step's tokens take.
+#include <type_traits>
+
 #include "attention.h"
 #include "kv_layout.h"
 
@@ -69,6 +72,21 @@ __device__ __forceinline__ void store8_at(void* base, int64_t elem, const float 
 #pragma unroll
     for (int i = 0; i < 8; ++i) b[i] = (__bf16)v[i];
     __builtin_nontemporal_store(__builtin_bit_cast(u32x4, b), reinterpret_cast<u32x4*>(reinterpret_cast<__bf16*>(base) + elem));
+  }
+}
+
+// The same to the caches: rows that the next kernel reads.
+template <bool F32>
+__device__ __forceinline__ void put8_at(void* base, int64_t elem, const float (&v)[8]) {
+  if constexpr (F32) {
+    f32x4* p = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(base) + elem);
+    p[0] = f32x4{v[0], v[1], v[2], v[3]};
+    p[1] = f32x4{v[4], v[5], v[6], v[7]};
+  } else {
+    bf16x8 b;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = (__bf16)v[i];
+    *reinterpret_cast<bf16x8*>(reinterpret_cast<__bf16*>(base) + elem) = b;
   }
 }
 
@@ -179,21 +197,177 @@ __device__ __forceinline__ uint32_t quad_transpose(uint32_t w, int k) {
   return k & 2 ? ((r >> 8) & 0x00FF00FFu) | (w & 0xFF00FF00u) : (w & 0x00FF00FFu) | ((r & 0x00FF00FFu) << 8);
 }
 
+// ---- rotary positions ------------------------------------------------------
+
+// Cosine and sine of an angle in 64 bits: reduced by multiples of pi/2 in two
+// parts (the first difference is exact up to 2^31 quarter turns), then the
+// series of both to the terms of 16th and 17th order, below 2^-60 at pi/4. So
+// far positions keep their angle, and the 32-bit numbers are the nearest ones
+// but for one case in 2^27.
+__device__ __forceinline__ void cos_sin(double angle, double& c, double& s) {
+  const double n = __builtin_rint(angle * 0.63661977236758134308);
+  const double r = __builtin_fma(-n, 6.123233995736765886e-17, __builtin_fma(-n, 1.57079632679489661923, angle));
+  const double x = r * r;
+  double p = 1.0 / 355687428096000.0;  // 1 / 17!
+  p = __builtin_fma(p, x, -1.0 / 1307674368000.0);
+  p = __builtin_fma(p, x, 1.0 / 6227020800.0);
+  p = __builtin_fma(p, x, -1.0 / 39916800.0);
+  p = __builtin_fma(p, x, 1.0 / 362880.0);
+  p = __builtin_fma(p, x, -1.0 / 5040.0);
+  p = __builtin_fma(p, x, 1.0 / 120.0);
+  p = __builtin_fma(p, x, -1.0 / 6.0);
+  const double si = __builtin_fma(p * x, r, r);
+  double q = 1.0 / 20922789888000.0;  // 1 / 16!
+  q = __builtin_fma(q, x, -1.0 / 87178291200.0);
+  q = __builtin_fma(q, x, 1.0 / 479001600.0);
+  q = __builtin_fma(q, x, -1.0 / 3628800.0);
+  q = __builtin_fma(q, x, 1.0 / 40320.0);
+  q = __builtin_fma(q, x, -1.0 / 720.0);
+  q = __builtin_fma(q, x, 1.0 / 24.0);
+  q = __builtin_fma(q, x, -0.5);
+  const double co = __builtin_fma(q, x, 1.0);
+  const int quarter = (int)(n - 4.0 * __builtin_floor(n * 0.25));
+  const double a = quarter & 1 ? si : co, b = quarter & 1 ? co : si;
+  c = quarter == 1 || quarter == 2 ? -a : a;
+  s = quarter >= 2 ? -b : b;
+}
+
+constexpr int kRopeTokens = 16;  // of a workgroup
+constexpr int64_t kRopeGroups = 1024;  // workgroups aimed at
+
+// Cosine and sine of the workgroup's tokens, [kRopeTokens][rotary / 2] of LDS:
+// once for all heads.
+__device__ __forceinline__ void rope_table(const RopeArgs& r, int64_t first, int tokens, const Div& half, f32x2* table) {
+  for (int n = threadIdx.x; n < tokens * (int)half.d; n += 256) {
+    const int t = (int)(((uint64_t)(uint32_t)n * half.m) >> half.shift), i = n - t * (int)half.d;
+    const int axis = r.axis != nullptr ? r.axis[i] : 0;
+    const int pos = (unsigned)axis < (unsigned)r.axes ? r.positions[axis * r.axis_stride + first + t] : 0;
+    double c, s;
+    cos_sin((double)pos * (double)r.inv_freq[i], c, s);
+    table[n] = f32x2{(float)(r.factor * c), (float)(r.factor * s)};
+  }
+}
+
+// fl(fl(x c) - fl(y s)) and fl(fl(y c) + fl(x s)): no fused product, so that a
+// key has the same bits whether it is turned here or with single operations.
+__device__ __forceinline__ float turn_first(float x, float y, f32x2 cs) {
+#pragma clang fp contract(off)
+  return x * cs[0] - y * cs[1];
+}
+__device__ __forceinline__ float turn_second(float x, float y, f32x2 cs) {
+#pragma clang fp contract(off)
+  return y * cs[0] + x * cs[1];
+}
+
+// A unit of a turned row: 8 channels and their partners (pairs of halves), or
+// 8 channels of 4 neighbouring pairs; units past those are copied.
+struct RopeUnits {
+  Div per_head, heads, half;
+};
+RopeUnits rope_units(const RopeArgs& r) {
+  const bool copies = r.x != r.out;
+  const int turned = r.neighbours ? r.rotary / 8 : r.rotary / 16, rest = copies ? (r.dim - r.rotary) / 8 : 0;
+  return {div_by((uint32_t)(turned + rest)), div_by((uint32_t)(r.heads > 0 ? r.heads : 1)), div_by((uint32_t)r.rotary / 2)};
+}
+__device__ __forceinline__ uint32_t div_n(uint32_t n, const Div& d) { return (uint32_t)(((uint64_t)n * d.m) >> d.shift); }
+
+// Part `part` of `parts` of the tokens' units.
+template <bool IN32, bool OUT32>
+__device__ __forceinline__ void rope_rows(const RopeArgs& r, const RopeUnits& units, int64_t first, int tokens, unsigned part,
+                                          unsigned parts, const f32x2* table) {
+  const uint32_t total = (uint32_t)tokens * units.heads.d * units.per_head.d;
+  const int half = r.rotary / 2;
+  for (uint32_t n = part * 256 + threadIdx.x; n < total; n += parts * 256) {
+    const uint32_t m = div_n(n, units.per_head), t = div_n(m, units.heads);
+    const int j = (int)(n - m * units.per_head.d), h = (int)(m - t * units.heads.d);
+    const int64_t from = (first + t) * r.x_stride + (int64_t)h * r.dim, to = (first + t) * r.out_stride + (int64_t)h * r.dim;
+    float x[8], y[8], a[8], b[8];
+    if (r.neighbours) {
+      load8_at<IN32>(r.x, from + 8 * j, x);
+      if (8 * j < r.rotary) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x2 cs = table[t * half + 4 * j + i];
+          a[2 * i] = turn_first(x[2 * i], x[2 * i + 1], cs);
+          a[2 * i + 1] = turn_second(x[2 * i], x[2 * i + 1], cs);
+        }
+        put8_at<OUT32>(r.out, to + 8 * j, a);
+      } else {
+        put8_at<OUT32>(r.out, to + 8 * j, x);
+      }
+    } else if (16 * j < r.rotary) {
+      load8_at<IN32>(r.x, from + 8 * j, x);
+      load8_at<IN32>(r.x, from + half + 8 * j, y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const f32x2 cs = table[t * half + 8 * j + i];
+        a[i] = turn_first(x[i], y[i], cs);
+        b[i] = turn_second(x[i], y[i], cs);
+      }
+      put8_at<OUT32>(r.out, to + 8 * j, a);
+      put8_at<OUT32>(r.out, to + half + 8 * j, b);
+    } else {
+      const int at = r.rotary / 2 + 8 * j;
+      load8_at<IN32>(r.x, from + at, x);
+      put8_at<OUT32>(r.out, to + at, x);
+    }
+  }
+}
+
+// Rows alone.
+template <bool IN32, bool OUT32>
+__global__ __launch_bounds__(256) void k_rope(RopeArgs r, RopeUnits units) {
+  __shared__ f32x2 table[kRopeTokens * 256];
+  const int64_t first = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * kRopeTokens;
+  if (first >= r.T) return;
+  const int tokens = r.T - first < kRopeTokens ? (int)(r.T - first) : kRopeTokens;
+  rope_table(r, first, tokens, units.half, table);
+  __syncthreads();
+  rope_rows<IN32, OUT32>(r, units, first, tokens, blockIdx.x, gridDim.x, table);
+}
+
+// Channels 8 j + [0, 8) of a key head at `from`, turned; `table`: its token's.
+template <bool F32>
+__device__ __forceinline__ void turn_key(const RopeArgs& r, const void* k, int64_t from, int j, const f32x2* table, float (&x)[8]) {
+  const int half = r.rotary / 2, at = 8 * j;
+  if (at >= r.rotary) return;
+  float y[8];
+  if (r.neighbours) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x2 cs = table[4 * j + i];
+      y[2 * i] = turn_first(x[2 * i], x[2 * i + 1], cs);
+      y[2 * i + 1] = turn_second(x[2 * i], x[2 * i + 1], cs);
+    }
+  } else {
+    const bool second = at >= half;
+    load8_at<F32>(k, second ? from - half : from + half, y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const f32x2 cs = table[second ? at - half + i : at + i];
+      y[i] = second ? turn_second(y[i], x[i], cs) : turn_first(x[i], y[i], cs);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = y[i];
+}
+
 // 8192 tokens of 8 heads of 128 (43 MB) take 10 to 12 us, bound by instruction
 // issue (two block scales with their exact divisions a lane) as much as by
 // memory; 64 tokens 3.8 us, the dependent trips: slots, rows, stores. Entries
 // of the list that fill an aligned quad of slots are written whole by the wave
 // that holds the first of them; any other entry's V shares its dwords with
 // tokens that another wave, or an earlier call, owns.
-template <int D, bool F32>
-__global__ __launch_bounds__(256) void k_kv_write(CacheArgs c, const void* k, const void* v, int64_t T, int64_t ks,
-                                                  int64_t vs, const int64_t* slots, const float* kg, const float* vg,
-                                                  Div groups) {
+// ROPE: `table` holds the cosines and sines of the workgroup's tokens.
+template <int D, bool F32, bool ROPE>
+__device__ __forceinline__ void write_units(const CacheArgs& c, const void* k, const void* v, int64_t T, int64_t ks, int64_t vs,
+                                            const int64_t* slots, const float* kg, const float* vg, const Div& groups,
+                                            unsigned chunk, const RopeArgs& r, const f32x2* table) {
   using R = KvRec<D>;
   const int lane = threadIdx.x & 63, row = lane >> 4;
   const int64_t first = (((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * 4 + (threadIdx.x >> 6)) * 4;
   if (first >= T) return;
-  const Unit<D> u = unit_at<D>(blockIdx.x * 16 + (lane & 15), c.heads);
+  const Unit<D> u = unit_at<D>(chunk * 16 + (lane & 15), c.heads);
   const int64_t t = first + row;
   // K's row is asked for together with the slots.
   float x[8];
@@ -206,6 +380,8 @@ __global__ __launch_bounds__(256) void k_kv_write(CacheArgs c, const void* k, co
   const uint32_t leads = (uint32_t)__ballot(s >= 0 && (s & 3) == 0 && s < c.pages * c.page_size) & runs & (runs >> 1) & (runs >> 2) & 0x7Fu;
   const Slot at = slot_at(__shfl(s, 3 + row), c.pages, groups);
   if (t < T && at.ok && u.ok) {  // both lanes of a K block
+    if constexpr (ROPE)
+      turn_key<F32>(r, k, t * ks + (int64_t)u.h * D + 8 * u.j, u.j, table + ((threadIdx.x >> 6) * 4 + row) * (r.rotary / 2), x);
     uint32_t sc;
     const uint32_t kc = quant8(x, *kg, sc);
     uint8_t* rec = c.cache + record_at<D>(at, c.heads, u.h, groups);
@@ -252,6 +428,33 @@ __global__ __launch_bounds__(256) void k_kv_write(CacheArgs c, const void* k, co
     }
     if (u.c4 < 2) rec[vs_at<D>(u, at.t >> 2) + 4 * u.c4 + (at.t & 3)] = (uint8_t)sc;
   }
+}
+
+template <int D, bool F32>
+__global__ __launch_bounds__(256) void k_kv_write(CacheArgs c, const void* k, const void* v, int64_t T, int64_t ks,
+                                                  int64_t vs, const int64_t* slots, const float* kg, const float* vg,
+                                                  Div groups) {
+  write_units<D, F32, false>(c, k, v, T, ks, vs, slots, kg, vg, groups, blockIdx.x, RopeArgs{}, nullptr);
+}
+
+// The first kv_parts workgroups of a group of tokens write its keys and values,
+// the others turn its queries.
+template <int D, bool F32, bool OUT32>
+__global__ __launch_bounds__(256) void k_rope_kv_write(RopeArgs r, RopeUnits units, CacheArgs c, const void* k, const void* v,
+                                                       int64_t ks, int64_t vs, const int64_t* slots, const float* kg,
+                                                       const float* vg, Div groups, unsigned kv_parts) {
+  __shared__ f32x2 table[kRopeTokens * D / 2];
+  const int64_t first = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * kRopeTokens;
+  if (first >= r.T) return;
+  const int tokens = r.T - first < kRopeTokens ? (int)(r.T - first) : kRopeTokens;
+  rope_table(r, first, tokens, units.half, table);
+  __syncthreads();
+  if (blockIdx.x >= kv_parts) {
+    rope_rows<F32, OUT32>(r, units, first, tokens, blockIdx.x - kv_parts, gridDim.x - kv_parts, table);
+    return;
+  }
+  for (unsigned chunk = blockIdx.x; chunk * 16 < (unsigned)c.heads * (D / 8); chunk += kv_parts)
+    write_units<D, F32, true>(c, k, v, r.T, ks, vs, slots, kg, vg, groups, chunk, r, table);
 }
 
 // 8 numbers of a code dword: fl(fl(q s) g).
@@ -312,6 +515,183 @@ __global__ __launch_bounds__(256) void k_kv_read(CacheArgs c, const int64_t* slo
   store4_at<F32>(v, to + 32 * u.m + 16 + 4 * u.c4, z + 4);
 }
 
+// ---- pages and slots ---------------------------------------------------------
+
+// All pages free, page 0 on top.
+__global__ __launch_bounds__(256) void k_kv_pool_reset(int32_t* pool, int64_t pages) {
+  for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < pages + kPoolHead; i += (int64_t)gridDim.x * 256)
+    pool[i] = i == 0 ? (int32_t)pages : i < kPoolHead ? 0 : (int32_t)(pages - 1 - (i - kPoolHead));
+}
+
+constexpr int kAdvanceThreads = 256, kAdvanceRows = 2048;  // of a workgroup
+
+// Sums of a request's rows, pages taken and pages given back. They stop at
+// 2^30: past T, the pool and a table's width nothing depends on their value.
+struct Sums {
+  uint32_t rows, taken, given;
+};
+__device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) {
+  const uint32_t s = a + b;
+  return s < (1u << 30) ? s : 1u << 30;
+}
+__device__ __forceinline__ Sums operator+(const Sums& a, const Sums& b) {
+  return {sat_add(a.rows, b.rows), sat_add(a.taken, b.taken), sat_add(a.given, b.given)};
+}
+
+// Requests in chunks of one a thread, with sums over those before. Every
+// workgroup goes over the requests for itself (they are few numbers, and read
+// only) and fills its rows; the last to arrive, when nobody reads them any
+// more, writes lengths, the pages that are given back and the pool. So one
+// launch does it all, a step of few rows in one workgroup.
+__global__ __launch_bounds__(kAdvanceThreads) void k_kv_advance(AdvanceArgs a, Div page) {
+  __shared__ Sums waves[kAdvanceThreads / 64];
+  __shared__ uint32_t end[kAdvanceThreads], begin[kAdvanceThreads], before[kAdvanceThreads], given_end[kAdvanceThreads];
+  __shared__ int old[kAdvanceThreads], held[kAdvanceThreads], first_gone[kAdvanceThreads];
+  __shared__ uint32_t popped, status, arrived;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int32_t* stack = a.pool + kPoolHead;
+  const int free = a.pool[0], top = free < 0 ? 0 : free > a.pages ? a.pages : free;
+  const uint32_t T = (uint32_t)a.T, row0 = blockIdx.x * kAdvanceRows, row1 = T - row0 < kAdvanceRows ? T : row0 + kAdvanceRows;
+  const int64_t room64 = (int64_t)a.table_width * a.page_size;
+  const int room = room64 < (1 << 30) ? (int)room64 : 1 << 30;
+  if (tid == 0) popped = status = 0;
+
+  struct Request {
+    int len;  // after the call
+    bool ok;
+  };
+  // The chunk's requests: their numbers in LDS, and the sums up to its end.
+  auto sweep = [&](int64_t chunk, Sums& sum) {
+    const int64_t b = chunk * kAdvanceThreads + tid;
+    int c = 0, was = 0;
+    if (b < a.B) {
+      c = a.counts[b];
+      was = a.seq_lens[b];
+    }
+    was = was < 0 ? 0 : was > 1 << 30 ? 1 << 30 : was;
+    const int64_t next = (int64_t)was + c;
+    const bool over = c > 0 && next > room;
+    const int now = next < 0 ? 0 : over ? was : (int)next;
+    int has = (int)div_n((uint32_t)was + page.d - 1, page), need = (int)div_n((uint32_t)now + page.d - 1, page);
+    has = has < a.table_width ? has : a.table_width;
+    need = need < a.table_width ? need : a.table_width;
+    const Sums own{c > 0 ? ((uint32_t)c < (1u << 30) ? (uint32_t)c : 1u << 30) : 0u, need > has ? (uint32_t)(need - has) : 0u,
+                   need < has ? (uint32_t)(has - need) : 0u};
+    Sums up = own;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const Sums x{(uint32_t)__shfl_up((int)up.rows, d), (uint32_t)__shfl_up((int)up.taken, d), (uint32_t)__shfl_up((int)up.given, d)};
+      if (lane >= d) up = up + x;
+    }
+    __syncthreads();  // what the chunk before left in LDS has been read
+    if (lane == 63) waves[wave] = up;
+    __syncthreads();
+    Sums base = sum;
+#pragma unroll
+    for (int w = 0; w < kAdvanceThreads / 64; ++w) {
+      if (w < wave) base = base + waves[w];
+      sum = sum + waves[w];
+    }
+    up = base + up;
+    const bool many = c > 0 && up.rows > T, lack = !many && own.taken > 0 && up.taken > (uint32_t)top;
+    Request q;
+    q.ok = !(over || many || lack);
+    q.len = q.ok ? now : was;
+    end[tid] = up.rows;
+    begin[tid] = up.rows - own.rows;
+    before[tid] = up.taken - own.taken;
+    given_end[tid] = up.given;
+    old[tid] = q.ok ? was : -1;
+    held[tid] = has;
+    first_gone[tid] = need;
+    if (own.taken > 0 && q.ok) atomicMax(&popped, up.taken);
+    const uint32_t bits = (lack ? 1u : 0u) | (over ? 2u : 0u) | (many ? 4u : 0u);
+    if (bits) atomicOr(&status, bits);
+    __syncthreads();
+    return q;
+  };
+  // The first of the chunk's requests whose sum passes n.
+  auto find = [&](const uint32_t* sums, uint32_t n) {
+    int lo = 0;
+#pragma unroll
+    for (int d = kAdvanceThreads / 2; d > 0; d /= 2)
+      if (sums[lo + d - 1] <= n) lo += d;
+    return lo;
+  };
+
+  const int64_t chunks = (a.B + kAdvanceThreads - 1) / kAdvanceThreads;
+  Sums sum{0, 0, 0};
+  Request mine{0, false};
+  for (int64_t chunk = 0; chunk < chunks; ++chunk) {
+    if (chunk > 0 && sum.rows >= row1) break;
+    const uint32_t from = sum.rows;
+    mine = sweep(chunk, sum);
+    const uint32_t to = sum.rows < row1 ? sum.rows : row1;
+    for (uint32_t t = (from > row0 ? from : row0) + tid; t < to; t += kAdvanceThreads) {
+      const int i = find(end, t);
+      const int64_t b = chunk * kAdvanceThreads + i;
+      int64_t slot = -1;
+      int position = 0;
+      if (old[i] >= 0) {
+        const int pos = old[i] + (int)(t - begin[i]), col = (int)div_n((uint32_t)pos, page), in = pos - col * (int)page.d;
+        int32_t* entry = a.table + b * a.table_stride + col;
+        int p;
+        if (col < held[i]) {
+          p = *entry;
+        } else {
+          p = stack[top - 1 - (int)before[i] - (col - held[i])];
+          if (in == 0) *entry = p;
+        }
+        slot = (int64_t)p * page.d + in;
+        position = a.offsets != nullptr ? pos + a.offsets[b] : pos;
+      }
+      if (a.slots != nullptr) a.slots[t] = slot;
+      if (a.positions != nullptr) a.positions[t] = position;
+    }
+  }
+  for (uint32_t t = (sum.rows > row0 ? sum.rows : row0) + tid; t < row1; t += kAdvanceThreads) {  // rows of no request
+    if (a.slots != nullptr) a.slots[t] = -1;
+    if (a.positions != nullptr) a.positions[t] = 0;
+  }
+
+  __syncthreads();
+  if (tid == 0) arrived = gridDim.x == 1 ? 0u : __hip_atomic_fetch_add(a.pool + 2, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  if (arrived != gridDim.x - 1) return;
+  if (chunks > 1) {  // sums over all requests
+    sum = {0, 0, 0};
+    for (int64_t chunk = 0; chunk < chunks; ++chunk) sweep(chunk, sum);
+  }
+  const int64_t left64 = (int64_t)top - popped + sum.given;
+  const int left = left64 < a.pages ? (int)left64 : a.pages;
+  sum = {0, 0, 0};
+  for (int64_t chunk = 0; chunk < chunks; ++chunk) {
+    const uint32_t from = sum.given;
+    if (chunks > 1) mine = sweep(chunk, sum);
+    else sum.given = given_end[kAdvanceThreads - 1];
+    const int64_t b = chunk * kAdvanceThreads + tid;
+    if (b < a.B) {
+      a.seq_lens[b] = mine.len;
+      if (a.q_offsets != nullptr) a.q_offsets[b + 1] = (int32_t)(end[tid] < T ? end[tid] : T);
+    }
+    // Pages come back so that a growth that is undone leaves the stack as it was.
+    for (uint32_t j = from + tid; j < sum.given; j += kAdvanceThreads) {
+      const int i = find(given_end, j);
+      const uint32_t i0 = i > 0 ? given_end[i - 1] : from;
+      int32_t* entry = a.table + (chunk * kAdvanceThreads + i) * a.table_stride + first_gone[i] + (j - i0);
+      const int at = left - 1 - (int)j;
+      if (at >= 0) stack[at] = *entry;
+      *entry = -1;
+    }
+  }
+  if (tid == 0) {
+    if (a.q_offsets != nullptr) a.q_offsets[0] = 0;
+    a.pool[0] = left;
+    if (status) a.pool[1] |= (int)status;
+    a.pool[2] = 0;
+  }
+}
+
 // x: 16 units of an entry; y, z: 16 entries.
 dim3 unit_grid(int64_t T, int heads, int dim) {
   const int64_t n = (T + 15) / 16, gy = n < 32768 ? n : 32768;
@@ -325,6 +705,28 @@ void write_d(const CacheArgs& c, const void* k, const void* v, bool f32, int64_t
   const Div groups = div_by((uint32_t)c.page_size / 16);
   if (f32) k_kv_write<D, true><<<grid, dim3(256), 0, s>>>(c, k, v, T, ks, vs, slots, kg, vg, groups);
   else k_kv_write<D, false><<<grid, dim3(256), 0, s>>>(c, k, v, T, ks, vs, slots, kg, vg, groups);
+}
+// Workgroups of a group of tokens over `items` of them: as many as fill the
+// chip, at most one an item.
+unsigned rope_parts(int64_t T, int64_t items) {
+  const int64_t groups = (T + kRopeTokens - 1) / kRopeTokens, want = (kRopeGroups + groups - 1) / groups;
+  return (unsigned)(items < 1 ? 0 : items < want ? items : want);
+}
+int64_t rope_items(const RopeArgs& r, const RopeUnits& units) {
+  const int64_t tokens = r.T < kRopeTokens ? r.T : kRopeTokens;
+  return (tokens * r.heads * units.per_head.d + 255) / 256;
+}
+
+template <int D, bool F32>
+void rope_write_d(const RopeArgs& r, const CacheArgs& c, const void* k, const void* v, int64_t ks, int64_t vs, const int64_t* slots,
+                  const float* kg, const float* vg, hipStream_t s) {
+  const RopeUnits units = rope_units(r);
+  dim3 grid = unit_grid(r.T, c.heads, D);
+  const unsigned kv_parts = rope_parts(r.T, grid.x);
+  grid.x = kv_parts + rope_parts(r.T, rope_items(r, units));
+  const Div groups = div_by((uint32_t)c.page_size / 16);
+  if (r.out_f32) k_rope_kv_write<D, F32, true><<<grid, dim3(256), 0, s>>>(r, units, c, k, v, ks, vs, slots, kg, vg, groups, kv_parts);
+  else k_rope_kv_write<D, F32, false><<<grid, dim3(256), 0, s>>>(r, units, c, k, v, ks, vs, slots, kg, vg, groups, kv_parts);
 }
 template <int D>
 void read_d(const CacheArgs& c, const int64_t* slots, int64_t T, const float* kg, const float* vg, void* k, void* v,
@@ -342,6 +744,42 @@ hipError_t launch_kv_write(const CacheArgs& c, const void* k, const void* v, boo
   if (c.dim == 64) write_d<64>(c, k, v, f32_in, T, k_stride, v_stride, slots, kg, vg, s);
   else if (c.dim == 128) write_d<128>(c, k, v, f32_in, T, k_stride, v_stride, slots, kg, vg, s);
   else write_d<256>(c, k, v, f32_in, T, k_stride, v_stride, slots, kg, vg, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_rope_kv_write(const RopeArgs& r, const CacheArgs& c, const void* k, const void* v, int64_t ks, int64_t vs,
+                                const int64_t* slots, const float* kg, const float* vg, hipStream_t s) {
+  auto go = [&](auto f32) {
+    constexpr bool F32 = decltype(f32)::value;
+    if (c.dim == 64) rope_write_d<64, F32>(r, c, k, v, ks, vs, slots, kg, vg, s);
+    else if (c.dim == 128) rope_write_d<128, F32>(r, c, k, v, ks, vs, slots, kg, vg, s);
+    else rope_write_d<256, F32>(r, c, k, v, ks, vs, slots, kg, vg, s);
+  };
+  if (r.x_f32) go(std::true_type{});
+  else go(std::false_type{});
+  return hipGetLastError();
+}
+
+hipError_t launch_rope(const RopeArgs& r, hipStream_t s) {
+  const RopeUnits units = rope_units(r);
+  dim3 grid = unit_grid(r.T, 1, 64);
+  grid.x = rope_parts(r.T, rope_items(r, units));
+  if (r.x_f32 && r.out_f32) k_rope<true, true><<<grid, dim3(256), 0, s>>>(r, units);
+  else if (r.x_f32) k_rope<true, false><<<grid, dim3(256), 0, s>>>(r, units);
+  else if (r.out_f32) k_rope<false, true><<<grid, dim3(256), 0, s>>>(r, units);
+  else k_rope<false, false><<<grid, dim3(256), 0, s>>>(r, units);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_pool_reset(int32_t* pool, int64_t pages, hipStream_t s) {
+  const int64_t n = (pages + kPoolHead + 255) / 256;
+  k_kv_pool_reset<<<dim3((unsigned)(n < 1024 ? n : 1024)), dim3(256), 0, s>>>(pool, pages);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_advance(const AdvanceArgs& a, hipStream_t s) {
+  const int n = (a.T + kAdvanceRows - 1) / kAdvanceRows;
+  k_kv_advance<<<dim3((unsigned)(n > 1 ? n : 1)), dim3(kAdvanceThreads), 0, s>>>(a, div_by((uint32_t)a.page_size));
   return hipGetLastError();
 }
 
