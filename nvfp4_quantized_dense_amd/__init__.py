@@ -603,12 +603,17 @@ def nvfp4_kv_read(cache, slots, k_g, v_g, k=None, v=None, dtype=torch.bfloat16, 
     return k, v
 
 
-def _same_gpu(*tensors):
+def _same_gpu(first, *others):
     """All of them (or None) on the current GPU, whose stream the call is on."""
-    here = torch._C._cuda_getDevice() if all(t is None or t.is_cuda for t in tensors) else _not_on_gpu()
-    for t in tensors:
-        if t is not None and t.get_device() != here:
-            raise ValueError(f"all tensors must be on the current GPU, cuda:{here}")
+    at = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != at:
+            at = min(at, t.get_device(), -1) if at < 0 or t.get_device() < 0 else None
+            break
+    if at is not None and at < 0:
+        _not_on_gpu()
+    if at is None or at != torch._C._cuda_getDevice():
+        raise ValueError(f"all tensors must be on the current GPU, cuda:{torch._C._cuda_getDevice()}")
 
 
 POOL_HEAD = 4  # words of a pool before its stack

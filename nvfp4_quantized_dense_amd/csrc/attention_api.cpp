@@ -137,7 +137,7 @@ int nvfp4_kv_read(const void* cache, int64_t pages, int64_t page_size, int64_t h
 static constexpr int64_t kAttnCounters = 1024;
 
 static int attn_sizes(int64_t T, int64_t B, int64_t heads_q, int64_t heads, int64_t head_dim, int64_t max_q,
-                      int64_t max_len, int64_t window, int64_t sinks, bool tree, nvfp4::AttnPlan& p) {
+                      int64_t max_len, int64_t window, int64_t sinks, bool tree, int64_t rows, nvfp4::AttnPlan& p) {
   int st = cache_sizes(1, 16, heads, head_dim);
   if (st) return st;
   if (heads_q < 1 || heads_q > 65536 || heads_q % heads != 0)
@@ -146,7 +146,11 @@ static int attn_sizes(int64_t T, int64_t B, int64_t heads_q, int64_t heads, int6
   if (max_len < 0 || max_len > (int64_t(1) << 30)) return fail(NVFP4_ERR_INVALID_ARG, "max_len must be 0 to 2^30");
   if (window < 0 || window > (int64_t(1) << 30)) return fail(NVFP4_ERR_INVALID_ARG, "window must be 0 to 2^30");
   if (sinks < 0 || sinks > (int64_t(1) << 30)) return fail(NVFP4_ERR_INVALID_ARG, "sinks must be 0 to 2^30");
-  p = nvfp4::attn_plan(B, (int)heads_q, (int)heads, (int)head_dim, max_q, max_len, window, sinks, tree);
+  if (sinks > 0 || tree) {
+    p = nvfp4::attn_masked_plan(B, (int)heads_q, (int)heads, (int)head_dim, max_q, max_len, window, sinks, tree, rows);
+  } else {
+    p = nvfp4::attn_plan(B, (int)heads_q, (int)heads, (int)head_dim, max_q, max_len, window);
+  }
   if (p.units > nvfp4::kAttnMaxUnits) return fail(NVFP4_ERR_INVALID_ARG, "too many sequences, heads and queries for one call");
   return NVFP4_OK;
 }
@@ -154,7 +158,7 @@ static int attn_sizes(int64_t T, int64_t B, int64_t heads_q, int64_t heads, int6
 size_t nvfp4_kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t heads_q, int64_t heads, int64_t head_dim,
                                           int64_t max_q, int64_t max_len) {
   nvfp4::AttnPlan p;
-  if (attn_sizes(T, B, heads_q, heads, head_dim, max_q, max_len, 0, 0, false, p)) return 0;
+  if (attn_sizes(T, B, heads_q, heads, head_dim, max_q, max_len, 0, 0, false, 0, p)) return 0;
   const int64_t floats = nvfp4::attn_workspace_floats(B, (int)heads_q, (int)heads, (int)head_dim, max_q, max_len);
   return kAttnCounters * sizeof(uint32_t) + align256((size_t)floats * sizeof(float));
 }
@@ -180,8 +184,9 @@ int nvfp4_kv_attention_masked(const uint16_t* q, int64_t q_stride, int64_t T, in
     return fail(NVFP4_ERR_INVALID_ARG, "out_dtype must be BF16 or F32");
   int st = cache_sizes(pages, page_size, heads, head_dim);
   if (st) return st;
+  if (window == 0 && sinks > 0 && sinks <= (int64_t(1) << 30)) sinks = 0;  // nothing to keep
   nvfp4::AttnPlan p;
-  st = attn_sizes(T, B, heads_q, heads, head_dim, max_q, max_len, window, sinks, tree != nullptr, p);
+  st = attn_sizes(T, B, heads_q, heads, head_dim, max_q, max_len, window, sinks, tree != nullptr, q_offsets ? T : 0, p);
   if (st) return st;
   if (tree) {
     if (max_q > nvfp4::kMaxTree || tree_words < (max_q + 63) / 64 || tree_words > nvfp4::kMaxTree / 64)
@@ -212,7 +217,7 @@ int nvfp4_kv_attention_masked(const uint16_t* q, int64_t q_stride, int64_t T, in
   a.q = q; a.q_stride = q_stride; a.T = T; a.B = B; a.heads_q = (int)heads_q; a.q_offsets = q_offsets; a.max_q = max_q;
   a.table = block_table; a.table_stride = table_stride; a.table_width = table_width; a.seq_lens = seq_lens;
   a.max_len = max_len; a.scale = scale; a.window = window;
-  a.sinks = window > 0 ? sinks : 0; a.tree = tree; a.tree_words = (int)tree_words; a.k_g = k_g; a.v_g = v_g; a.out = out;
+  a.sinks = sinks; a.tree = tree; a.tree_words = (int)tree_words; a.k_g = k_g; a.v_g = v_g; a.out = out;
   a.f32_out = out_dtype == NVFP4_DTYPE_F32; a.lse = lse;
   a.counters = static_cast<uint32_t*>(ws);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kAttnCounters * sizeof(uint32_t));

@@ -117,7 +117,12 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
   // grid: (head, row block, sequence) fastest to slowest in x, split in y
   const unsigned unit = blockIdx.x, heads = a.c.heads, blocks = p.row_blocks;
   const int h = (int)(unit % heads);
-  const unsigned rb = unit / heads % blocks, b = unit / heads / blocks;
+  unsigned rb = unit / heads % blocks, b = unit / heads / blocks;
+  if (MASKED && p.packed) {
+    const Block at = packed_block(a, p, unit, G, lane);
+    b = at.b;
+    rb = at.rb;
+  }
   const int split = blockIdx.y;
 
   // Without a window the page numbers of this split can be asked for before
@@ -264,19 +269,27 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
-// The join of split units by a kernel of its own: 1024 / D / kSlices rows a
-// workgroup, a thread four channels of every kSlices-th run of kRun splits. In
+// The join of split units by a kernel of its own: 1024 / D / SLICES rows a
+// workgroup, a thread four channels of every SLICES-th run of kRun splits. In
 // the order of the runs, whatever the timing. In one workgroup a unit (the
 // last to arrive) it took 64 rows 5 us a split; so, spread over the chip and
-// with 8 loads in flight a thread, about 5 us in all.
-template <int D, bool MASKED>
+// with 8 loads in flight a thread, about 5 us in all. One slice where a run
+// holds all splits: with four, three of them idle, 512 units of 64 rows of 64
+// channels took 19 us for two splits.
+constexpr int kRun = 8;
+template <int D, int SLICES, bool MASKED>
 __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, AttnPlan p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int kSlices = 4, kRun = 8, kThreads = D / 4, kRowsHere = 256 / kThreads / kSlices;
+  constexpr int kSlices = SLICES, kThreads = D / 4, kRowsHere = 256 / kThreads / kSlices;
   const int G = a.heads_q / a.c.heads, rows_wg = p.rows;
   const unsigned unit = blockIdx.x, heads = a.c.heads, blocks = p.row_blocks;
   const int h = (int)(unit % heads);
-  const unsigned rb = p.tiled ? blocks - 1 - unit / heads % blocks : unit / heads % blocks, b = unit / heads / blocks;
+  unsigned rb = p.tiled ? blocks - 1 - unit / heads % blocks : unit / heads % blocks, b = unit / heads / blocks;
+  if (MASKED && p.packed) {
+    const Block at = packed_block(a, p, unit, G, threadIdx.x & 63);
+    b = at.b;
+    rb = at.rb;
+  }
   const Seq seq = seq_of(a, b, G);
   const int slot = threadIdx.x / kThreads, slice = slot % kSlices, d = threadIdx.x % kThreads * 4;
   const int rr = blockIdx.y * kRowsHere + slot / kSlices;
@@ -314,23 +327,27 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, AttnPlan p) {
       }
     }
   }
-  __shared__ f32x4 jv[256];
-  __shared__ float jm[256], jl[256];
-  jm[threadIdx.x] = m;
-  jl[threadIdx.x] = l;
-  jv[threadIdx.x] = v;
-  __syncthreads();
-  if (slice != 0 || row0 + rr >= seq.rows) return;
+  if constexpr (kSlices > 1) {
+    __shared__ f32x4 jv[256];
+    __shared__ float jm[256], jl[256];
+    jm[threadIdx.x] = m;
+    jl[threadIdx.x] = l;
+    jv[threadIdx.x] = v;
+    __syncthreads();
+    if (slice != 0 || row0 + rr >= seq.rows) return;
 #pragma unroll
-  for (int z = 1; z < kSlices; ++z) m = __builtin_fmaxf(m, jm[threadIdx.x + z * kThreads]);
-  l = 0.0f;
-  v = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int z = 1; z < kSlices; ++z) m = __builtin_fmaxf(m, jm[threadIdx.x + z * kThreads]);
+    l = 0.0f;
+    v = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int z = 0; z < kSlices; ++z) {
-    const int at = threadIdx.x + z * kThreads;
-    const float w = __builtin_amdgcn_exp2f(jm[at] - m);
-    l += w * jl[at];
-    v += jv[at] * w;
+    for (int z = 0; z < kSlices; ++z) {
+      const int at = threadIdx.x + z * kThreads;
+      const float w = __builtin_amdgcn_exp2f(jm[at] - m);
+      l += w * jl[at];
+      v += jv[at] * w;
+    }
+  } else if (row0 + rr >= seq.rows) {
+    return;
   }
   const int64_t orow = out_row(a, seq, row0 + rr, h, G);
   store4(a, orow * D + d, v * inverse_sum(l, *a.v_g));
@@ -340,11 +357,12 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, AttnPlan p) {
 
 // The rows of a drafted tree's mask from its parents, a thread a row: it walks
 // up its ancestors, whose numbers only fall, so that the words are finished
-// from the last to the first. A chain of LDS reads as long as the row is deep.
+// from the last to the first. What bounds it is the chain of LDS reads: a read
+// gives four ancestors.
 constexpr int kTreeThreads = 256;
 __global__ __launch_bounds__(kTreeThreads) void k_tree_mask(TreeArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  __shared__ int parent[kMaxTree];
+  __shared__ struct alignas(8) { int16_t up[4]; } above[kMaxTree];  // ancestors 1 to 4 steps up, or -1
   const int64_t b = blockIdx.x;
   int64_t q0 = b * a.max_q, n = a.max_q;
   if (a.q_offsets != nullptr) {
@@ -357,22 +375,42 @@ __global__ __launch_bounds__(kTreeThreads) void k_tree_mask(TreeArgs a) {
   const int row0 = (int)blockIdx.y * kTreeThreads, i = row0 + (int)threadIdx.x;
   if (row0 >= n) return;
   const int first = a.positions != nullptr ? a.positions[q0] : 0;
-  for (int at = threadIdx.x; at < row0 + kTreeThreads && at < n; at += kTreeThreads) {
+  const int rows = row0 + kTreeThreads < n ? row0 + kTreeThreads : (int)n;
+  for (int at = threadIdx.x; at < rows; at += kTreeThreads) {
     const int p = a.parents[q0 + at];
-    parent[at] = p < at ? p : -1;
+    above[at].up[0] = (int16_t)(p >= 0 && p < at ? p : -1);
+  }
+  __syncthreads();
+  for (int at = threadIdx.x; at < rows; at += kTreeThreads) {
+    const int p = above[at].up[0];
+    above[at].up[1] = p < 0 ? (int16_t)-1 : above[p].up[0];
+  }
+  __syncthreads();
+  for (int at = threadIdx.x; at < rows; at += kTreeThreads) {
+    const int p = above[at].up[1];
+    above[at].up[2] = p < 0 ? (int16_t)-1 : above[p].up[0];
+    above[at].up[3] = p < 0 ? (int16_t)-1 : above[p].up[1];
   }
   __syncthreads();
   if (i >= n) return;
   uint64_t* out = a.tree + (q0 + i) * a.tree_words;
   int word = a.tree_words - 1, depth = -1;
   uint64_t bits = 0;
-  for (int at = i; at >= 0; at = parent[at]) {
+  auto take = [&](int at) {
+    if (at < 0) return;
     for (; word > at >> 6; --word) {
       out[word] = bits;
       bits = 0;
     }
     bits |= uint64_t(1) << (at & 63);
     ++depth;
+  };
+  for (int at = i; at >= 0;) {
+    const auto next = above[at];
+    take(at);
+#pragma unroll
+    for (int x = 0; x < 3; ++x) take(next.up[x]);
+    at = next.up[3];
   }
   for (; word >= 0; --word) {
     out[word] = bits;
@@ -400,11 +438,16 @@ void launch_stream(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
     launch_parts<D, 1, false>(a, p, s);
   }
 }
+template <int D, int SLICES>
+void launch_slices(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+  const dim3 grid((unsigned)p.units, (unsigned)(p.rows * D / (1024 / SLICES)));
+  if (attn_masked(a)) k_kv_join<D, SLICES, true><<<grid, dim3(256), 0, s>>>(a, p);
+  else k_kv_join<D, SLICES, false><<<grid, dim3(256), 0, s>>>(a, p);
+}
 template <int D>
 void launch_join(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
-  const dim3 grid((unsigned)p.units, (unsigned)(p.rows * D / 256));
-  if (attn_masked(a)) k_kv_join<D, true><<<grid, dim3(256), 0, s>>>(a, p);
-  else k_kv_join<D, false><<<grid, dim3(256), 0, s>>>(a, p);
+  if (p.splits <= kRun) launch_slices<D, 1>(a, p, s);
+  else launch_slices<D, 4>(a, p, s);
 }
 
 }  // namespace

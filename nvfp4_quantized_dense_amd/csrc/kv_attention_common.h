@@ -227,6 +227,29 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, unsigned b, int G) {
   s.len = len > room ? (int)room : len;
   return s;
 }
+// The sequence and the row block of a unit. Later rows of a sequence see more
+// keys: they come first. Packed blocks' sequence is found by a wave's lanes at
+// once among 64 offsets.
+struct Block {
+  unsigned b, rb;
+};
+__device__ __forceinline__ Block packed_block(const AttnArgs& a, const AttnPlan& p, unsigned unit, int G, int lane) {
+  const unsigned n = (unsigned)p.row_blocks - 1 - unit / (unsigned)a.c.heads;
+  unsigned b = 0, at = n + 1;  // in front of the first sequence: no row block
+  for (int64_t b0 = 0; b0 < a.B; b0 += 64) {
+    const int64_t i = b0 + lane < a.B ? b0 + lane : a.B - 1;
+    const int first = a.q_offsets[i];
+    // (Offsets are at most T < 2^24, a kv head's rows under 2^31; others are no sequence's.)
+    const int64_t s = attn_first_block(first < 0 ? 0 : first, i, G, p.rows);
+    const unsigned before = (unsigned)__popcll(__ballot(b0 + lane < a.B && s <= (int64_t)n));
+    if (before == 0) break;
+    b = (unsigned)b0 + before - 1;
+    at = (unsigned)__shfl((int)s, (int)before - 1);
+    if (before < 64) break;
+  }
+  return {(unsigned)__builtin_amdgcn_readfirstlane(b), n - (unsigned)__builtin_amdgcn_readfirstlane(at)};
+}
+
 // Query i stands at position len - nq + i and sees [lo, hi).
 __device__ __forceinline__ int sees_hi(const Seq& s, int i) {
   const int64_t e = (int64_t)s.len - s.nq + i + 1;

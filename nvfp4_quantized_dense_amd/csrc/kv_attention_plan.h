@@ -4,6 +4,7 @@
 #pragma once
 #include <stdint.h>
 
+#include <cmath>
 #include <initializer_list>
 
 namespace nvfp4 {
@@ -16,20 +17,27 @@ struct AttnPlan {
   int row_tiles;    // 16-row tiles per workgroup, tiled: per wave
   int64_t units;    // row_blocks * B * heads
   int rows;         // of a workgroup
-  int row_blocks;   // per (sequence, head)
+  int row_blocks;   // per (sequence, head), or packed: per head
+  bool packed;      // row blocks by the queries' offsets: attn_first_block
   int chunk;        // keys per split
   int splits;       // most splits of one unit
   int part_floats;  // per (unit, split)
 };
 constexpr int attn_tile_max(int dim) { return dim == 64 ? 4 : 2; }  // most row tiles of a wave
 
+// Where the row blocks of a sequence whose queries begin at `first` begin, if it
+// is sequence b: in order and apart, as many as it needs at least, and no more
+// than T * G / rows + B in all. By B * max_q, a ragged batch's workgroups are
+// mostly without rows, and go to CUs for nothing: 16 trees of 3 to 61 tokens,
+// of 512 workgroups 284 with rows, had these on 172 of 256 CUs.
+constexpr int64_t attn_first_block(int64_t first, int64_t b, int G, int rows) { return first * G / rows + b; }
+
 // Workgroups of many rows that run at once; of few rows, the number aimed at
 // (at most); keys of a split (at least, tiled and not); splits of a unit (at most).
 constexpr int64_t attn_tile_slots(int dim) { return dim == 256 ? 256 : 512; }
 constexpr int64_t kAttnSlots = 1024, kAttnTileKeys = 256, kAttnKeys = 512, kAttnMaxSplits = 256;
 
-inline AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t max_q, int64_t max_len, int64_t window,
-                          int64_t sinks = 0, bool tree = false) {
+inline AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t max_q, int64_t max_len, int64_t window) {
   AttnPlan p{};
   const int64_t G = heads_q / heads, rows = max_q * G;
   int64_t per, slots;  // rows of a workgroup, workgroups that fill the chip
@@ -41,7 +49,7 @@ inline AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t ma
     // Few workgroups: smaller ones, unless their rows pay for the keys' second
     // making (8 heads, group 8: 16 x 16000 keys 28.2 us with 64 rows, 32.4 with
     // 128; 128 tokens x 8192 keys 66 and 58 us).
-    const int64_t keys = window > 0 && window + 64 + sinks < max_len ? window + 64 + sinks : max_len;
+    const int64_t keys = window > 0 && window + 64 < max_len ? window + 64 : max_len;
     if (blocks * B * heads < slots && (keys <= 2048 || rows <= 512)) blocks = (rows + 63) / 64;
     p.row_tiles = (int)((rows + 64 * blocks - 1) / (64 * blocks));
     per = 64 * p.row_tiles;
@@ -60,15 +68,13 @@ inline AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t ma
   p.rows = (int)per;
   p.part_floats = (int)per * (dim + 2);
   // Keys that a unit reads at most, from a multiple of 32 on: its rows are of
-  // at most (per - 1) / G + 2 queries, or all see a tree's last key, and the
-  // sinks are walked in front of it. (With a window the more splits for all
+  // at most (per - 1) / G + 2 queries. (With a window the more splits for all
   // max_q queries' keys are mostly empty: 1000 tokens of 2 sequences, 20 heads
   // on 4, window 128 take 24 us so, 51 with those.)
   int64_t span = max_len;
   int64_t queries = (per - 1) / G + 2;
-  if (queries > max_q || tree) queries = max_q;
-  const int64_t head = (sinks + 31) / 32 * 32;
-  if (window > 0 && head + window + queries + 30 < span) span = head + window + queries + 30;
+  if (queries > max_q) queries = max_q;
+  if (window > 0 && window + queries + 30 < span) span = window + queries + 30;
   span = (span + 31) / 32 * 32;
   // At least 512 keys a split: one token of 4 sequences of 8000 keys 15.4 us
   // so, 21.1 with 256 (16 heads of 128 a kv head). Tiled 256, as a workgroup
@@ -109,14 +115,94 @@ inline AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t ma
   return p;
 }
 
+// What a call of the masked kernels costs by workgroups of `rows` rows: `fixed`
+// us, per key of a workgroup sqrt(alone^2 + (shared n)^2) ns where the busiest
+// CU has n workgroups, and with splits `join` us and the partials out and in at
+// `tbs` TB/s. Fitted to calls of trees and windows with sinks (66 sizes, 1 to 64
+// splits each); what it chooses took 1.03 times as long as the best split
+// measured of the same size in the mean, 1.16 at most.
+struct AttnCost {
+  int rows;
+  double fixed, alone, shared, join, tbs;
+};
+constexpr AttnCost kAttnCosts[3][5] = {
+    {{16, 5.9, 4.6, 3.6, 0.5, 3.2}, {32, 8.2, 6.1, 3.9, 3.8, 2.9}, {64, 10.8, 15.9, 8.1, 0.8, 4.5}, {128, 11.9, 19.6, 12.4, 0.5, 4.8},
+     {256, 11.0, 34.8, 23.7, 2.9, 4.9}},
+    {{16, 5.5, 2.9, 6.8, 1.3, 4.5}, {32, 16.6, 4.6, 5.6, 0.5, 3.1}, {64, 14.5, 15.9, 12.0, 0.5, 4.1}, {128, 15.7, 21.2, 15.9, 0.5, 4.7}, {}},
+    {{16, 5.9, 1.0, 11.8, 0.5, 3.6}, {32, 22.8, 1.0, 14.1, 1.2, 2.1}, {64, 16.6, 11.5, 33.5, 0.5, 3.4}, {128, 21.1, 15.0, 43.6, 0.5, 4.3}, {}}};
+
+// The split of a call with sinks or a tree's mask. T: rows of all sequences, 0
+// if each has max_q. A workgroup of few rows streams keys at a lower cost a key,
+// one of many shares the making of f16 among its rows: whichever is estimated
+// to end first. (By the rule above 16 trees of 3 to 61 tokens of 8 heads of 64
+// a kv head, window 2000, took 71 us, 39 so; 4 of 64 tokens over 65536 keys,
+// 64 heads of 128 on 8, 874 and 601.)
+inline AttnPlan attn_masked_plan(int64_t B, int heads_q, int heads, int dim, int64_t max_q, int64_t max_len, int64_t window,
+                                 int64_t sinks, bool tree, int64_t T) {
+  const int64_t G = heads_q / heads, rows = max_q * G, head = (sinks + 31) / 32 * 32;
+  AttnPlan best{};
+  double least_cost = 0.0;
+  for (const AttnCost& c : kAttnCosts[dim == 64 ? 0 : dim == 128 ? 1 : 2]) {
+    // 16 rows where there are no more, else 32 and, for more than 64, multiples of 64.
+    if (c.rows == 0 || (c.rows == 16) != (rows <= 16) || (c.rows > 32 && rows <= 64)) continue;
+    AttnPlan p{};
+    p.tiled = c.rows > 32;
+    p.rows = c.rows;
+    p.row_tiles = p.tiled ? c.rows / 64 : c.rows / 16;
+    p.part_floats = c.rows * (dim + 2);
+    int64_t blocks = (rows + c.rows - 1) / c.rows;
+    p.units = blocks * B * heads;
+    if (T > 0 && B <= 512 && 4 * (T * G / c.rows + B) <= 3 * blocks * B) {
+      p.packed = true;
+      blocks = T * G / c.rows + B;
+      p.units = blocks * heads;
+    }
+    if (p.units > kAttnMaxUnits) {
+      if (best.units == 0 || best.units > kAttnMaxUnits) best = p;
+      continue;
+    }
+    p.row_blocks = (int)blocks;
+    // Keys that a unit walks over at most: those of its rows' queries (a tree's
+    // all see its last key), from a multiple of 32 on, and the sinks.
+    int64_t span = max_len, queries = (c.rows - 1) / G + 2;
+    if (queries > max_q || tree) queries = max_q;
+    if (window > 0 && head + window + queries + 30 < span) span = head + window + queries + 30;
+    span = (span + 31) / 32 * 32;
+    const int64_t least = p.tiled ? kAttnTileKeys : kAttnKeys;
+    int64_t most = (span + least - 1) / least;
+    if (most > kAttnMaxSplits) most = kAttnMaxSplits;
+    // Splits that fill the CUs n times over, as they go: units * splits <= 1024.
+    for (int n = 0; n <= 4; ++n) {
+      int64_t want = p.units > 0 && n > 0 ? n * 256 / p.units : 1;
+      if (want > most) want = most;
+      if (want < 1) want = 1;
+      p.chunk = (int)(((span + want - 1) / want + 127) / 128 * 128);
+      if (p.chunk < 128) p.chunk = 128;
+      p.splits = span > 0 ? (int)((span + p.chunk - 1) / p.chunk) : 1;
+      const double keys = (double)(p.chunk < span ? p.chunk : span), wgs = (double)p.units * p.splits;
+      const double busiest = (double)((p.units * p.splits + 255) / 256) * c.shared;
+      double cost = c.fixed + 1e-3 * keys * std::sqrt(c.alone * c.alone + busiest * busiest);
+      if (p.splits > 1) cost += c.join + 8e-6 * wgs * p.part_floats / c.tbs;
+      if (best.row_blocks == 0 || cost < least_cost) {
+        best = p;
+        least_cost = cost;
+      }
+    }
+  }
+  return best;
+}
+
 // Floats of the partials of any call of at most B sequences, max_q queries of
-// each and max_len keys, with any window, sinks and trees: at least units * splits * part_floats
-// of all their plans that split, and itself never less for larger sizes.
+// each and max_len keys, with any window, sinks and trees: at least
+// units * splits * part_floats of all their plans that split, and itself never less for larger sizes.
 //   Few rows: splits <= slots / units rounded up, slots <= kAttnSlots, so
 //   units * splits < units + kAttnSlots, and units < kAttnSlots or splits = 1.
 //   Tiled, S = attn_tile_slots: splits <= (r + 3) S / units, r = units / S
 //   rounded up, so units * splits <= units + 4 S; two splits or more need
 //   (r + 3) S >= 2 units > 2 (r - 1) S, thus r <= 4 and units * splits <= 7 S.
+//   Masked: units * splits <= 1024 = kAttnSlots <= 4 S. Workgroups of 32 of
+//   more than 64 rows are twice as many as of 64, with half the splits at most;
+//   of 128 rows of 64 channels half as many rows as in blocks of 256.
 // No unit has more splits than its keys give.
 inline int64_t attn_workspace_floats(int64_t B, int heads_q, int heads, int dim, int64_t max_q, int64_t max_len) {
   const int64_t rows = max_q * (heads_q / heads), groups = B * heads;

@@ -47,9 +47,17 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
   // Later rows see more keys: they start first.
   const unsigned unit = blockIdx.x, heads = a.c.heads, blocks = p.row_blocks;
   const int h = (int)(unit % heads);
-  const unsigned rb = blocks - 1 - unit / heads % blocks, b = unit / heads / blocks;
+  unsigned rb = blocks - 1 - unit / heads % blocks, b = unit / heads / blocks;
+  if (MASKED && p.packed) {
+    const Block at = packed_block(a, p, unit, G, lane);
+    b = at.b;
+    rb = at.rb;
+  }
   const int split = blockIdx.y;
 
+  // As in kv_attention.hip: page numbers are asked for before the lengths where
+  // they do not depend on them, and the first two tiles before the query rows.
+  Walk<D> walk(a, b, h, a.window > 0 ? 0 : split * (p.chunk / 16), lane);
   const Seq seq = seq_of(a, b, G);
   if ((int64_t)rb * kRows >= seq.rows) return;
   const int row0 = (int)rb * kRows;
@@ -59,6 +67,36 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
   const int s_first = all.start + split * p.chunk;
   const int s_last = all.end - s_first > p.chunk ? s_first + p.chunk : all.end;
   const int tiles = s_last > s_first ? (s_last - s_first + kTile - 1) / kTile : 0;
+
+  // Wave w brings K of the tile's record w and half w & 1 of V's channels of
+  // the pair w >> 1.
+  const int pair = wave >> 1, half = wave & 1;
+  KFrag<D> fk, nk;  // of the tile at hand, of the one after the first
+  VFrag<D, 2> fv[2], nv[2];
+  bool ok[2] = {true, true}, nok[2] = {true, true};
+  int ahead = s_first + 32 * pair;  // the next of this wave's pairs fetched
+  bool jump = ahead < all.head;
+  auto fetch = [&](KFrag<D>& k, VFrag<D, 2> (&v)[2], bool (&okay)[2]) {
+    if constexpr (MASKED) {
+      if (jump && ahead >= all.head) {
+        walk.start((ahead + all.gap) >> 4);
+        jump = false;
+      }
+      ahead += kTile;
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const Rsrc rec = walk.record(okay[x], lane);
+      load_v(v[x], rec, lane, half);
+      if (x == half) load_k(k, rec, lane);
+      walk.step(x == 0 ? 1 : 3);
+    }
+  };
+  if (tiles > 0) {
+    walk.start(all.key<MASKED>(ahead) >> 4);
+    fetch(fk, fv, ok);
+    fetch(nk, nv, nok);
+  }
 
   Rows<D, RT> r;
   const int wrow0 = row0 + wave * 16 * RT;
@@ -73,12 +111,6 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
     } else lo_full = sees_lo(sees_hi(seq, (seq.rows < wrow0 + 16 * RT ? seq.rows - 1 : wrow0 + 16 * RT - 1) / G), a.window);
   }
 
-  // Wave w brings K of the tile's record w and half w & 1 of V's channels of
-  // the pair w >> 1.
-  const int pair = wave >> 1, half = wave & 1;
-  KFrag<D> fk;
-  VFrag<D, 2> fv[2];
-  bool ok[2] = {true, true};
   // Before what was fetched becomes operands: tokens no row sees may never
   // have been written. Their V scales become zero, so that no NaN code meets
   // a zero probability. `base`: the tile's first place.
@@ -172,33 +204,17 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
     if (lane == 0) page_ok[buf][wave] = ok[half];
   };
   if (tiles > 0) {
-    Walk<D> walk(a, b, h, s_first >> 4, lane);
-    int ahead = s_first + 32 * pair;  // the next of this wave's pairs fetched
-    walk.start(all.key<MASKED>(ahead) >> 4);
-    bool jump = ahead < all.head;
-    auto fetch = [&] {
-      if constexpr (MASKED) {
-        if (jump && ahead >= all.head) {
-          walk.start((ahead + all.gap) >> 4);
-          jump = false;
-        }
-        ahead += kTile;
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const Rsrc rec = walk.record(ok[x], lane);
-        load_v(fv[x], rec, lane, half);
-        if (x == half) load_k(fk, rec, lane);
-        walk.step(x == 0 ? 1 : 3);
-      }
-    };
-    fetch();
     clear_v(s_first);
     make_tile(0, 0);
-    fetch();
+    fk = nk;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      fv[x] = nv[x];
+      ok[x] = nok[x];
+    }
     clear_v(s_first + kTile);
     make_tile(1, 1);
-    fetch();
+    fetch(fk, fv, ok);
     __syncthreads();
     f32x4 sa[RT][2], sb[RT][2];
     float mx[RT];
@@ -227,7 +243,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
       attend(sb, sa, mx, 4 * (buf ^ 1) * kW, kV2 + third * kB, [&](auto n) { put(n, buf, third2); });
       if (lane == 0) page_ok[buf][wave] = ok[half];
       oks = __builtin_amdgcn_readfirstlane(flags);
-      fetch();
+      fetch(fk, fv, ok);
       third = third == 2 ? 0 : third + 1;
     }
   }

@@ -233,7 +233,10 @@ __device__ __forceinline__ void cos_sin(double angle, double& c, double& s) {
 }
 
 constexpr int kRopeTokens = 16;  // of a workgroup
-constexpr int64_t kRopeGroups = 1024;  // workgroups aimed at
+// Workgroups aimed at: 8192 tokens of 40 heads of 128 in halves / half of the
+// channels / neighbouring pairs 49 / 50 / 51 us, 49 / 53 / 55 with 1024 (each
+// makes its tokens' table for itself).
+constexpr int64_t kRopeGroups = 512;
 
 // Cosine and sine of the workgroup's tokens, [kRopeTokens][rotary / 2] of LDS:
 // once for all heads.
@@ -259,15 +262,18 @@ __device__ __forceinline__ float turn_second(float x, float y, f32x2 cs) {
   return y * cs[0] + x * cs[1];
 }
 
-// A unit of a turned row: 8 channels and their partners (pairs of halves), or
-// 8 channels of 4 neighbouring pairs; units past those are copied.
+// Units of a row: 8 channels and their partners half a rotation on, 8 channels
+// of 4 neighbouring pairs, or 8 channels that only move. Each kind has a loop
+// of its own, as a branch within a wave waits for both sides' loads: with half
+// of the channels turned, 8192 tokens of 40 heads of 128 took 66 us in one.
 struct RopeUnits {
-  Div per_head, heads, half;
+  Div turned, rest, heads, half;  // units of a head
+  bool copies;
 };
 RopeUnits rope_units(const RopeArgs& r) {
-  const bool copies = r.x != r.out;
-  const int turned = r.neighbours ? r.rotary / 8 : r.rotary / 16, rest = copies ? (r.dim - r.rotary) / 8 : 0;
-  return {div_by((uint32_t)(turned + rest)), div_by((uint32_t)(r.heads > 0 ? r.heads : 1)), div_by((uint32_t)r.rotary / 2)};
+  const int rest = (r.dim - r.rotary) / 8;
+  return {div_by((uint32_t)(r.neighbours ? r.rotary / 8 : r.rotary / 16)), div_by((uint32_t)(rest > 0 ? rest : 1)),
+          div_by((uint32_t)(r.heads > 0 ? r.heads : 1)), div_by((uint32_t)r.rotary / 2), rest > 0 && r.x != r.out};
 }
 __device__ __forceinline__ uint32_t div_n(uint32_t n, const Div& d) { return (uint32_t)(((uint64_t)n * d.m) >> d.shift); }
 
@@ -275,42 +281,65 @@ __device__ __forceinline__ uint32_t div_n(uint32_t n, const Div& d) { return (ui
 template <bool IN32, bool OUT32>
 __device__ __forceinline__ void rope_rows(const RopeArgs& r, const RopeUnits& units, int64_t first, int tokens, unsigned part,
                                           unsigned parts, const f32x2* table) {
-  const uint32_t total = (uint32_t)tokens * units.heads.d * units.per_head.d;
+  const uint32_t rows = (uint32_t)tokens * units.heads.d;
   const int half = r.rotary / 2;
-  for (uint32_t n = part * 256 + threadIdx.x; n < total; n += parts * 256) {
-    const uint32_t m = div_n(n, units.per_head), t = div_n(m, units.heads);
-    const int j = (int)(n - m * units.per_head.d), h = (int)(m - t * units.heads.d);
-    const int64_t from = (first + t) * r.x_stride + (int64_t)h * r.dim, to = (first + t) * r.out_stride + (int64_t)h * r.dim;
-    float x[8], y[8], a[8], b[8];
-    if (r.neighbours) {
-      load8_at<IN32>(r.x, from + 8 * j, x);
-      if (8 * j < r.rotary) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f32x2 cs = table[t * half + 4 * j + i];
-          a[2 * i] = turn_first(x[2 * i], x[2 * i + 1], cs);
-          a[2 * i + 1] = turn_second(x[2 * i], x[2 * i + 1], cs);
-        }
-        put8_at<OUT32>(r.out, to + 8 * j, a);
-      } else {
-        put8_at<OUT32>(r.out, to + 8 * j, x);
-      }
-    } else if (16 * j < r.rotary) {
-      load8_at<IN32>(r.x, from + 8 * j, x);
-      load8_at<IN32>(r.x, from + half + 8 * j, y);
+  struct Place {
+    int64_t from, to;
+    int t, j;
+  };
+  auto place = [&](uint32_t n, const Div& per_head) {
+    const uint32_t m = div_n(n, per_head), t = div_n(m, units.heads);
+    const int h = (int)(m - t * units.heads.d);
+    return Place{(first + t) * r.x_stride + (int64_t)h * r.dim, (first + t) * r.out_stride + (int64_t)h * r.dim, (int)t,
+                 (int)(n - m * per_head.d)};
+  };
+  const uint32_t begin = part * 256 + threadIdx.x, step = parts * 256;
+  if (!r.neighbours) {
+    for (uint32_t n = begin; n < rows * units.turned.d; n += step) {
+      const Place p = place(n, units.turned);
+      float x[8], y[8], a[8], b[8];
+      load8_at<IN32>(r.x, p.from + 8 * p.j, x);
+      load8_at<IN32>(r.x, p.from + half + 8 * p.j, y);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const f32x2 cs = table[t * half + 8 * j + i];
+        const f32x2 cs = table[p.t * half + 8 * p.j + i];
         a[i] = turn_first(x[i], y[i], cs);
         b[i] = turn_second(x[i], y[i], cs);
       }
-      put8_at<OUT32>(r.out, to + 8 * j, a);
-      put8_at<OUT32>(r.out, to + half + 8 * j, b);
-    } else {
-      const int at = r.rotary / 2 + 8 * j;
-      load8_at<IN32>(r.x, from + at, x);
-      put8_at<OUT32>(r.out, to + at, x);
+      put8_at<OUT32>(r.out, p.to + 8 * p.j, a);
+      put8_at<OUT32>(r.out, p.to + half + 8 * p.j, b);
     }
+  } else {
+    for (uint32_t n = begin; n < rows * units.turned.d; n += 2 * step) {  // two units at a time, for as many loads in flight
+      const uint32_t n2 = n + step;
+      const bool two = n2 < rows * units.turned.d;
+      const Place p[2] = {place(n, units.turned), place(two ? n2 : n, units.turned)};
+      float x[2][8], a[8];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) load8_at<IN32>(r.x, p[u].from + 8 * p[u].j, x[u]);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x2 cs = table[p[u].t * half + 4 * p[u].j + i];
+          a[2 * i] = turn_first(x[u][2 * i], x[u][2 * i + 1], cs);
+          a[2 * i + 1] = turn_second(x[u][2 * i], x[u][2 * i + 1], cs);
+        }
+        if (u == 0 || two) put8_at<OUT32>(r.out, p[u].to + 8 * p[u].j, a);
+      }
+    }
+  }
+  if (!units.copies) return;
+  for (uint32_t n = begin; n < rows * units.rest.d; n += 2 * step) {
+    const uint32_t n2 = n + step;
+    const bool two = n2 < rows * units.rest.d;
+    const Place p[2] = {place(n, units.rest), place(two ? n2 : n, units.rest)};
+    float x[2][8];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) load8_at<IN32>(r.x, p[u].from + r.rotary + 8 * p[u].j, x[u]);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (u == 0 || two) put8_at<OUT32>(r.out, p[u].to + r.rotary + 8 * p[u].j, x[u]);
   }
 }
 
@@ -523,7 +552,6 @@ __global__ __launch_bounds__(256) void k_kv_pool_reset(int32_t* pool, int64_t pa
     pool[i] = i == 0 ? (int32_t)pages : i < kPoolHead ? 0 : (int32_t)(pages - 1 - (i - kPoolHead));
 }
 
-constexpr int kAdvanceThreads = 256, kAdvanceRows = 2048;  // of a workgroup
 
 // Sums of a request's rows, pages taken and pages given back. They stop at
 // 2^30: past T, the pool and a table's width nothing depends on their value.
@@ -543,7 +571,11 @@ __device__ __forceinline__ Sums operator+(const Sums& a, const Sums& b) {
 // only) and fills its rows; the last to arrive, when nobody reads them any
 // more, writes lengths, the pages that are given back and the pool. So one
 // launch does it all, a step of few rows in one workgroup.
-__global__ __launch_bounds__(kAdvanceThreads) void k_kv_advance(AdvanceArgs a, Div page) {
+template <int N>
+constexpr int kAdvanceRowsOf = 8 * N;  // rows of a workgroup of N threads
+template <int N>
+__global__ __launch_bounds__(N) void k_kv_advance(AdvanceArgs a, Div page) {
+  constexpr int kAdvanceThreads = N, kAdvanceRows = kAdvanceRowsOf<N>;
   __shared__ Sums waves[kAdvanceThreads / 64];
   __shared__ uint32_t end[kAdvanceThreads], begin[kAdvanceThreads], before[kAdvanceThreads], given_end[kAdvanceThreads];
   __shared__ int old[kAdvanceThreads], held[kAdvanceThreads], first_gone[kAdvanceThreads];
@@ -560,14 +592,17 @@ __global__ __launch_bounds__(kAdvanceThreads) void k_kv_advance(AdvanceArgs a, D
     int len;  // after the call
     bool ok;
   };
+  int next_count, next_len;  // of the chunk to come, asked for a chunk ahead
+  auto ask = [&](int64_t chunk) {
+    const int64_t b = chunk * kAdvanceThreads + tid;
+    next_count = b < a.B ? a.counts[b] : 0;
+    next_len = b < a.B ? a.seq_lens[b] : 0;
+  };
   // The chunk's requests: their numbers in LDS, and the sums up to its end.
   auto sweep = [&](int64_t chunk, Sums& sum) {
-    const int64_t b = chunk * kAdvanceThreads + tid;
-    int c = 0, was = 0;
-    if (b < a.B) {
-      c = a.counts[b];
-      was = a.seq_lens[b];
-    }
+    const int c = next_count;
+    int was = next_len;
+    ask(chunk + 1);
     was = was < 0 ? 0 : was > 1 << 30 ? 1 << 30 : was;
     const int64_t next = (int64_t)was + c;
     const bool over = c > 0 && next > room;
@@ -622,31 +657,52 @@ __global__ __launch_bounds__(kAdvanceThreads) void k_kv_advance(AdvanceArgs a, D
   const int64_t chunks = (a.B + kAdvanceThreads - 1) / kAdvanceThreads;
   Sums sum{0, 0, 0};
   Request mine{0, false};
-  for (int64_t chunk = 0; chunk < chunks; ++chunk) {
+  int64_t swept = 0;
+  ask(0);
+  for (; swept < chunks; ++swept) {
+    const int64_t chunk = swept;
     if (chunk > 0 && sum.rows >= row1) break;
     const uint32_t from = sum.rows;
     mine = sweep(chunk, sum);
     const uint32_t to = sum.rows < row1 ? sum.rows : row1;
-    for (uint32_t t = (from > row0 ? from : row0) + tid; t < to; t += kAdvanceThreads) {
-      const int i = find(end, t);
-      const int64_t b = chunk * kAdvanceThreads + i;
-      int64_t slot = -1;
-      int position = 0;
-      if (old[i] >= 0) {
-        const int pos = old[i] + (int)(t - begin[i]), col = (int)div_n((uint32_t)pos, page), in = pos - col * (int)page.d;
-        int32_t* entry = a.table + b * a.table_stride + col;
-        int p;
-        if (col < held[i]) {
-          p = *entry;
-        } else {
-          p = stack[top - 1 - (int)before[i] - (col - held[i])];
-          if (in == 0) *entry = p;
-        }
-        slot = (int64_t)p * page.d + in;
-        position = a.offsets != nullptr ? pos + a.offsets[b] : pos;
+    // Four rows of a thread at a time without a branch, so that their searches
+    // and their page numbers are on their way together.
+    constexpr int kRows = 4;
+    for (uint32_t t0 = (from > row0 ? from : row0) + tid; t0 < to; t0 += kRows * kAdvanceThreads) {
+      uint32_t t[kRows];
+      int i[kRows], position[kRows], p[kRows], in[kRows], shift[kRows];
+      int32_t* entry[kRows];
+      bool live[kRows], comes[kRows];
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        t[u] = t0 + u * kAdvanceThreads;
+        i[u] = 0;
       }
-      if (a.slots != nullptr) a.slots[t] = slot;
-      if (a.positions != nullptr) a.positions[t] = position;
+#pragma unroll
+      for (int d = kAdvanceThreads / 2; d > 0; d /= 2)
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) i[u] += end[i[u] + d - 1] <= t[u] ? d : 0;
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        const int was = old[i[u]];
+        live[u] = t[u] < to && was >= 0;
+        const int pos = live[u] ? was + (int)(t[u] - begin[i[u]]) : 0, col = (int)div_n((uint32_t)pos, page);
+        const int64_t b = chunk * kAdvanceThreads + (live[u] ? i[u] : 0);
+        in[u] = pos - col * (int)page.d;
+        entry[u] = a.table + b * a.table_stride + col;
+        comes[u] = live[u] && col >= held[i[u]];
+        position[u] = pos;
+        const int32_t* at = comes[u] ? stack + (top - 1 - (int)before[i[u]] - (col - held[i[u]])) : entry[u];
+        p[u] = *(live[u] ? at : a.pool);
+        shift[u] = a.offsets != nullptr ? a.offsets[b] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        if (t[u] >= to) continue;
+        if (comes[u] && in[u] == 0) *entry[u] = p[u];
+        if (a.slots != nullptr) a.slots[t[u]] = live[u] ? (int64_t)p[u] * page.d + in[u] : -1;
+        if (a.positions != nullptr) a.positions[t[u]] = live[u] ? position[u] + shift[u] : 0;
+      }
     }
   }
   for (uint32_t t = (sum.rows > row0 ? sum.rows : row0) + tid; t < row1; t += kAdvanceThreads) {  // rows of no request
@@ -658,13 +714,11 @@ __global__ __launch_bounds__(kAdvanceThreads) void k_kv_advance(AdvanceArgs a, D
   if (tid == 0) arrived = gridDim.x == 1 ? 0u : __hip_atomic_fetch_add(a.pool + 2, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
   if (arrived != gridDim.x - 1) return;
-  if (chunks > 1) {  // sums over all requests
-    sum = {0, 0, 0};
-    for (int64_t chunk = 0; chunk < chunks; ++chunk) sweep(chunk, sum);
-  }
+  for (; swept < chunks; ++swept) sweep(swept, sum);  // sums over all requests
   const int64_t left64 = (int64_t)top - popped + sum.given;
   const int left = left64 < a.pages ? (int)left64 : a.pages;
   sum = {0, 0, 0};
+  ask(0);
   for (int64_t chunk = 0; chunk < chunks; ++chunk) {
     const uint32_t from = sum.given;
     if (chunks > 1) mine = sweep(chunk, sum);
@@ -714,7 +768,7 @@ unsigned rope_parts(int64_t T, int64_t items) {
 }
 int64_t rope_items(const RopeArgs& r, const RopeUnits& units) {
   const int64_t tokens = r.T < kRopeTokens ? r.T : kRopeTokens;
-  return (tokens * r.heads * units.per_head.d + 255) / 256;
+  return (tokens * r.heads * units.turned.d + 255) / 256;
 }
 
 template <int D, bool F32>
@@ -778,8 +832,10 @@ hipError_t launch_kv_pool_reset(int32_t* pool, int64_t pages, hipStream_t s) {
 }
 
 hipError_t launch_kv_advance(const AdvanceArgs& a, hipStream_t s) {
-  const int n = (a.T + kAdvanceRows - 1) / kAdvanceRows;
-  k_kv_advance<<<dim3((unsigned)(n > 1 ? n : 1)), dim3(kAdvanceThreads), 0, s>>>(a, div_by((uint32_t)a.page_size));
+  const Div page = div_by((uint32_t)a.page_size);
+  auto groups = [&](int rows) { return dim3((unsigned)(a.T > rows ? (a.T + rows - 1) / rows : 1)); };
+  if (a.B <= 256) k_kv_advance<256><<<groups(kAdvanceRowsOf<256>), dim3(256), 0, s>>>(a, page);
+  else k_kv_advance<1024><<<groups(kAdvanceRowsOf<1024>), dim3(1024), 0, s>>>(a, page);
   return hipGetLastError();
 }
 

@@ -179,7 +179,7 @@ def scan(tmp_path_factory):
 
 @pytest.mark.parametrize("seed", range(3))
 def test_masked_plans_fit(scan, seed):
-    at, used = (ctypes.c_int64 * 9)(), ctypes.c_int64()
+    at, used = (ctypes.c_int64 * 10)(), ctypes.c_int64()
     bad = scan(seed, 200000, at, ctypes.byref(used))
     assert bad == 0, (bad, list(at))
     assert used.value > 1000  # plans that skip keys and split were among them
