@@ -115,21 +115,34 @@ inline AttnPlan attn_plan(int64_t B, int heads_q, int heads, int dim, int64_t ma
   return p;
 }
 
-// What a call of the masked kernels costs by workgroups of `rows` rows: `fixed`
-// us, per key of a workgroup sqrt(alone^2 + (shared n)^2) ns where the busiest
-// CU has n workgroups, and with splits `join` us and the partials out and in at
-// `tbs` TB/s. Fitted to calls of trees and windows with sinks (66 sizes, 1 to 64
-// splits each); what it chooses took 1.03 times as long as the best split
-// measured of the same size in the mean, 1.16 at most.
+// What a call of the masked kernels costs by workgroups of `rows` rows, of which
+// a CU holds `slots`: `fixed` us; a key of n workgroups that share each CU
+// sqrt(alone^2 + (shared n)^2) ns, one round of full CUs after the other, the
+// last of fewer at least 0.55 of a full one's; with splits `join` us and the
+// partials out and in at `tbs` TB/s. Fitted to calls of trees and windows with
+// sinks (66 sizes, 1 to 64 splits each): what it chooses took 1.015 times as
+// long as the best split measured of the same size in the mean, 1.13 at most.
 struct AttnCost {
-  int rows;
+  int rows, slots;
   double fixed, alone, shared, join, tbs;
 };
 constexpr AttnCost kAttnCosts[3][5] = {
-    {{16, 5.9, 4.6, 3.6, 0.5, 3.2}, {32, 8.2, 6.1, 3.9, 3.8, 2.9}, {64, 10.8, 15.9, 8.1, 0.8, 4.5}, {128, 11.9, 19.6, 12.4, 0.5, 4.8},
-     {256, 11.0, 34.8, 23.7, 2.9, 4.9}},
-    {{16, 5.5, 2.9, 6.8, 1.3, 4.5}, {32, 16.6, 4.6, 5.6, 0.5, 3.1}, {64, 14.5, 15.9, 12.0, 0.5, 4.1}, {128, 15.7, 21.2, 15.9, 0.5, 4.7}, {}},
-    {{16, 5.9, 1.0, 11.8, 0.5, 3.6}, {32, 22.8, 1.0, 14.1, 1.2, 2.1}, {64, 16.6, 11.5, 33.5, 0.5, 3.4}, {128, 21.1, 15.0, 43.6, 0.5, 4.3}, {}}};
+    {{16, 4, 6.0, 4.8, 3.3, 0.5, 3.1}, {32, 3, 8.4, 6.9, 3.0, 3.4, 2.8}, {64, 4, 11.8, 15.5, 7.5, 0.5, 4.9},
+     {128, 3, 12.6, 19.9, 11.2, 0.5, 5.3}, {256, 2, 10.8, 37.1, 19.5, 3.9, 5.8}},
+    {{16, 3, 5.6, 3.9, 6.5, 1.0, 4.4}, {32, 2, 16.8, 4.8, 5.2, 0.5, 3.2}, {64, 2, 15.3, 17.3, 9.2, 0.5, 4.3},
+     {128, 2, 17.0, 22.2, 13.2, 0.5, 5.1}, {}},
+    {{16, 2, 5.7, 5.2, 11.0, 0.5, 3.2}, {32, 1, 22.8, 13.2, 5.2, 1.2, 2.1}, {64, 1, 16.9, 31.0, 16.4, 0.5, 3.6},
+     {128, 1, 21.3, 39.2, 24.0, 0.5, 4.5}, {}}};
+inline double attn_cost(const AttnCost& c, double keys, int64_t wgs, bool split, int part_floats) {
+  auto key = [&](double n) { return std::sqrt(c.alone * c.alone + c.shared * c.shared * n * n); };
+  const int64_t round = 256 * c.slots, last = wgs % round;
+  double ns = (double)(wgs / round) * key(c.slots);
+  if (last > 0) {
+    const double t = key((double)((last + 255) / 256)), most = 0.55 * c.shared * c.slots;
+    ns += wgs > round && t < most ? most : t;
+  }
+  return c.fixed + 1e-3 * keys * ns + (split ? c.join + 8e-6 * (double)wgs * part_floats / c.tbs : 0.0);
+}
 
 // The split of a call with sinks or a tree's mask. T: rows of all sequences, 0
 // if each has max_q. A workgroup of few rows streams keys at a lower cost a key,
@@ -179,10 +192,7 @@ inline AttnPlan attn_masked_plan(int64_t B, int heads_q, int heads, int dim, int
       p.chunk = (int)(((span + want - 1) / want + 127) / 128 * 128);
       if (p.chunk < 128) p.chunk = 128;
       p.splits = span > 0 ? (int)((span + p.chunk - 1) / p.chunk) : 1;
-      const double keys = (double)(p.chunk < span ? p.chunk : span), wgs = (double)p.units * p.splits;
-      const double busiest = (double)((p.units * p.splits + 255) / 256) * c.shared;
-      double cost = c.fixed + 1e-3 * keys * std::sqrt(c.alone * c.alone + busiest * busiest);
-      if (p.splits > 1) cost += c.join + 8e-6 * wgs * p.part_floats / c.tbs;
+      const double cost = attn_cost(c, (double)(p.chunk < span ? p.chunk : span), p.units * p.splits, p.splits > 1, p.part_floats);
       if (best.row_blocks == 0 || cost < least_cost) {
         best = p;
         least_cost = cost;
