@@ -1,7 +1,7 @@
 """One decoder layer on NVFP4 operators, served: prompts in ragged chunks, then
-one token of each sequence a step.
+one token of each sequence a step, or a drafted tree of each.
 
-    python examples/decoder_layer.py [--hidden 5120 --steps 32]
+    python examples/decoder_layer.py [--hidden 5120 --steps 32] [--draft 8 --window 4096 --sinks 4]
 
 Weights are random. The norm quantizes for the products, the projections' keys
 and values go into the paged NVFP4 cache as they are (slices of one output),
@@ -11,7 +11,10 @@ attention reads the cache, and the MLP half follows:
          -> NVFP4 -> output product -> r + ., norm, NVFP4
          -> gate_up product, SwiGLU, NVFP4 -> down product
 
-Rotary embedding and sampling are the caller's.
+With rope_theta queries and keys are turned by their positions on the way into
+the cache. Batch deals pages on the host; DeviceBatch does so on the GPU, so that
+a step can be captured with its bookkeeping, and drafts trees. Sampling is the
+caller's.
 """
 import argparse
 import os
@@ -25,10 +28,17 @@ import nvfp4_quantized_dense_amd as nv  # noqa: E402
 
 
 class DecoderLayer:
-    def __init__(self, hidden, inter, heads_q, heads, head_dim, pages, page_size, window=0, h_amax=8.0, seed=0, device="cuda"):
+    def __init__(self, hidden, inter, heads_q, heads, head_dim, pages, page_size, window=0, h_amax=8.0, seed=0, device="cuda",
+                 sinks=0, rope_theta=None, rope_sections=None):
         gen = torch.Generator(device).manual_seed(seed)
         self.hidden, self.inter, self.heads_q, self.heads, self.dim = hidden, inter, heads_q, heads, head_dim
-        self.page_size, self.window = page_size, window
+        self.page_size, self.window, self.sinks = page_size, window, sinks
+        self.inv_freq = self.axes = None
+        if rope_theta is not None:
+            half = torch.arange(head_dim // 2, dtype=torch.float64) / (head_dim // 2)
+            self.inv_freq = (rope_theta ** -half).float().to(device)
+            if rope_sections is not None:  # frequencies of each axis: time, height, width
+                self.axes = nv.nvfp4_rope_axes(rope_sections, device=device)
 
         def weight(rows, cols, kind=nv.REPACK_PLAIN):
             w = torch.randn(rows, cols, generator=gen, device=device) * cols ** -0.5
@@ -58,18 +68,23 @@ class DecoderLayer:
             self.ws = torch.zeros(need, dtype=torch.uint8, device=self.ws.device)
         return self.ws
 
-    def __call__(self, x, residual, slots, block_table, seq_lens, q_offsets, max_q, max_len, trace=None):
-        """x, residual bf16 [T, hidden] (residual is updated in place) -> bf16 [T, hidden]."""
+    def __call__(self, x, residual, slots, block_table, seq_lens, q_offsets, max_q, max_len, trace=None, positions=None, tree=None):
+        """x, residual bf16 [T, hidden] (residual is updated in place) -> bf16 [T, hidden]. positions int32 [T] or
+        [axes, T], where the layer turns; tree: the queries are drafted trees."""
         T, Hq, H, D = x.shape[0], self.heads_q, self.heads, self.dim
         codes, scales, residual, row_g = nv.add_rmsnorm_nvfp4_quant_per_token(x, self.norm1, residual=residual,
                                                                                residual_out=residual)
         qkv = nv.nvfp4_gemm_rowscale(codes, scales, row_g, self.w_qkv, (Hq + 2 * H) * D, self.hidden, self.g_qkv,
                                      out_dtype=torch.bfloat16)
         q, k, v = (part.unflatten(1, (-1, D)) for part in qkv.split([Hq * D, H * D, H * D], 1))
-        nv.nvfp4_kv_write(k, v, slots, self.kv_g_inv, self.kv_g_inv, self.cache)
+        if self.inv_freq is not None:
+            q = nv.nvfp4_rope_kv_write(q, k, v, positions, self.inv_freq, slots, self.kv_g_inv, self.kv_g_inv, self.cache,
+                                       axes=self.axes, q_out=q)
+        else:
+            nv.nvfp4_kv_write(k, v, slots, self.kv_g_inv, self.kv_g_inv, self.cache)
         ws = self.workspace(T, seq_lens.numel(), Hq, H, D, max_q, max_len)
         attn = nv.nvfp4_kv_attention(q, self.cache, block_table, seq_lens, self.kv_g, self.kv_g, q_offsets=q_offsets,
-                                     max_q=max_q, max_len=max_len, window=self.window, ws=ws)
+                                     max_q=max_q, max_len=max_len, window=self.window, ws=ws, sinks=self.sinks, tree=tree)
         a_codes, a_scales, a_g = nv.nvfp4_quantize_per_token(attn.view(T, Hq * D))
         o = nv.nvfp4_gemm_rowscale(a_codes, a_scales, a_g, self.w_o, self.hidden, Hq * D, self.g_o,
                                    out_dtype=torch.bfloat16)
@@ -113,6 +128,41 @@ class Batch:
                     q_offsets=torch.tensor(offsets, **i32), max_q=max(counts), max_len=self.max_len)
 
 
+class DeviceBatch:
+    """Sequences whose lengths, block tables and pool of pages stay on the GPU: nothing of a step depends on the host but
+    its number of rows, and a refused sequence is seen in `status`."""
+
+    def __init__(self, layer, sequences, max_len):
+        self.layer, self.max_len, dev = layer, max_len, layer.cache.device
+        self.lens = torch.zeros(sequences, dtype=torch.int32, device=dev)
+        self.table = torch.full((sequences, -(-max_len // layer.page_size)), -1, dtype=torch.int32, device=dev)
+        self.pool = nv.nvfp4_kv_pool(layer.cache.shape[0], device=dev)
+        self.status = self.pool[1:2]
+
+    def advance(self, counts, tokens, max_q, parents=None):
+        """Room for counts[b] (int32 on the GPU) more tokens of sequence b, `tokens` rows in all, at most max_q of one
+        sequence: the arguments of a layer call for them. parents (int32 [tokens]): they are drafted trees."""
+        slots, positions, offsets = nv.nvfp4_kv_advance(counts, self.lens, self.table, self.pool, self.layer.page_size, tokens)
+        tree = None
+        if parents is not None:
+            tree = nv.nvfp4_tree_mask(parents, offsets, max_q, positions=positions)
+        return dict(slots=slots, block_table=self.table, seq_lens=self.lens, q_offsets=offsets, max_q=max_q, max_len=self.max_len,
+                    positions=positions, tree=tree)
+
+    def accept(self, call, kept, counts, dropped):
+        """After a drafted call: its rows `kept` (int64, each sequence's accepted ones in order, counts[b] of them) become
+        the sequence's next tokens, and dropped[b] = tokens drafted - counts[b] are taken back."""
+        layer = self.layer
+        k, v = nv.nvfp4_kv_read(layer.cache, call["slots"][kept], layer.kv_g, layer.kv_g, dtype=torch.float32)
+        first = call["q_offsets"][:-1].long()
+        place = torch.arange(kept.numel(), device=kept.device)
+        begin = torch.cumsum(counts, 0) - counts
+        seq = torch.repeat_interleave(counts.long(), output_size=kept.numel())
+        to = call["slots"][first[seq] + place - begin[seq]]
+        nv.nvfp4_kv_write(k, v, to, layer.kv_g_inv, layer.kv_g_inv, layer.cache)
+        nv.nvfp4_kv_advance(-dropped, self.lens, self.table, self.pool, layer.page_size, 0)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--hidden", type=int, default=5120)
@@ -122,7 +172,12 @@ def main():
     ap.add_argument("--head-dim", type=int, default=128)
     ap.add_argument("--prompts", type=int, nargs="+", default=[1000, 37, 512, 1])
     ap.add_argument("--steps", type=int, default=32)
+    ap.add_argument("--draft", type=int, default=0, help="drafted tokens of a sequence a step, as a tree; 0: single tokens")
+    ap.add_argument("--window", type=int, default=0)
+    ap.add_argument("--sinks", type=int, default=0)
     a = ap.parse_args()
+    if a.draft:
+        return serve_trees(a)
     B, page = len(a.prompts), 64
     max_len = max(a.prompts) + a.steps
     layer = DecoderLayer(a.hidden, a.inter, a.heads_q, a.heads, a.head_dim, B * -(-max_len // page), page)
@@ -144,6 +199,48 @@ def main():
         assert bool(out.isfinite().all())
     print(f"prompts {a.prompts}, then {a.steps} steps of {B} tokens: {sorted(times)[len(times) // 2] * 1e6:.0f} us a step "
           f"(median, one layer), cache {layer.cache.numel() / 2 ** 20:.1f} MiB")
+
+
+def serve_trees(a):
+    """Prompts, then drafted trees of which each step accepts the path to a random leaf."""
+    B, n, page, dev = len(a.prompts), a.draft, 64, "cuda"
+    max_len = max(a.prompts) + (a.steps + 1) * n
+    layer = DecoderLayer(a.hidden, a.inter, a.heads_q, a.heads, a.head_dim, B * -(-max_len // page), page, window=a.window,
+                         sinks=a.sinks, rope_theta=1e6)
+    batch = DeviceBatch(layer, B, max_len)
+
+    def rows(m):
+        return torch.randn(m, a.hidden, device=dev).to(torch.bfloat16)
+
+    T = sum(a.prompts)
+    layer(rows(T), rows(T), **batch.advance(torch.tensor(a.prompts, dtype=torch.int32, device=dev), T, max(a.prompts)))
+    draft = torch.full((B,), n, dtype=torch.int32, device=dev)
+    times, accepted = [], 0
+    for _ in range(a.steps):
+        trees = [[-1] + [int(torch.randint(0, i, (1,))) for i in range(1, n)] for _ in range(B)]
+        parents = torch.tensor(sum(trees, []), dtype=torch.int32, device=dev)
+        x, r = rows(B * n), rows(B * n)
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        call = batch.advance(draft, B * n, n, parents)
+        out = layer(x, r, **call)
+        torch.cuda.synchronize()
+        times.append(time.perf_counter() - t0)
+        assert bool(out.isfinite().all())
+        kept, counts = [], []
+        for b, tree in enumerate(trees):
+            path, at = [], int(torch.randint(0, n, (1,)))
+            while at >= 0:
+                path.append(b * n + at)
+                at = tree[at]
+            kept += path[::-1]
+            counts.append(len(path))
+        counts = torch.tensor(counts, dtype=torch.int32, device=dev)
+        batch.accept(call, torch.tensor(kept, device=dev), counts, draft - counts)
+        accepted += len(kept)
+    assert int(batch.status) == 0
+    print(f"prompts {a.prompts}, then {a.steps} steps of {B} trees of {n} tokens: {sorted(times)[len(times) // 2] * 1e6:.0f} us a "
+          f"step (median, one layer), {accepted / a.steps / B:.2f} tokens accepted of a tree, lengths {batch.lens.tolist()}")
 
 
 if __name__ == "__main__":

@@ -104,9 +104,6 @@ struct AttnArgs {
   int64_t max_len;
   float scale;
   int64_t window;            // 0: none
-  int64_t sinks;             // first keys that stay visible behind a window
-  const uint64_t* tree;      // [T, tree_words] drafted keys a query sees, or null: causal
-  int tree_words;
   const float* k_g;
   const float* v_g;
   void* out;                 // [T, heads_q, dim] bf16 or f32
@@ -114,6 +111,9 @@ struct AttnArgs {
   float* lse;                // [T, heads_q] or null
   float* part;               // split partials
   uint32_t* counters;        // one per (row block, head, sequence), zero
+  int64_t sinks;             // first keys that stay visible behind a window
+  const uint64_t* tree;      // [T, tree_words] drafted keys a query sees, or null: causal
+  int tree_words;
 };
 // Whether a call needs the masked kernels.
 inline bool attn_masked(const AttnArgs& a) { return a.sinks > 0 || a.tree != nullptr; }

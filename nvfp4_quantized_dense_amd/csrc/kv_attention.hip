@@ -172,7 +172,7 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
   Rows<D, RT> r;
   load_rows<D, RT, MASKED>(r, a, seq, row0, h, G, quad, col);
   auto attend = [&](Pair& f, int base) {
-    const bool edge = needs_mask<MASKED>(a, base, lo_full, hi_full) || !f.ok[0] || !f.ok[1];
+    const bool edge = (MASKED ? masked_edge(a, base, lo_full, hi_full) : base + 32 > hi_full || base < lo_full) || !f.ok[0] || !f.ok[1];
     f32x4 sc[RT][2];
 #pragma unroll
     for (int t = 0; t < RT; ++t) sc[t][0] = sc[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -193,7 +193,7 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
       // Tokens no row sees may never have been written: their V scales
       // become zero, so that no NaN code meets a zero probability.
 #pragma unroll
-      for (int x = 0; x < 2; ++x) f.v[x].s &= f.ok[x] ? seen_bytes<MASKED>(a, all, base + 16 * x + 4 * quad) : 0u;
+      for (int x = 0; x < 2; ++x) f.v[x].s &= f.ok[x] ? (MASKED ? masked_bytes(a, base + 16 * x + 4 * quad, all.lo, all.hi) : byte_mask(base + 16 * x + 4 * quad, all.lo, all.hi)) : 0u;
     }
     f16x8 pf[P][RT];
     float mx[RT];

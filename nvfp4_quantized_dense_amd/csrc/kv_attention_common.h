@@ -156,6 +156,7 @@ struct Walk {
     const int at = tab0 + lane;
     if (last >= 0) tab = table[at < last ? at : last];
   }
+  Walk() = default;
   // The table from group g on.
   __device__ __forceinline__ Walk(const AttnArgs& a, unsigned b, int h, int g, int lane) {
     groups = a.c.page_size / 16;
@@ -450,19 +451,16 @@ __device__ __forceinline__ void hide_masked(const Rows<D, RT>& r, const AttnArgs
   }
 }
 
-// Whether a wave's step of 32 keys needs the mask: [lo_full, hi_full) and the
-// sinks are seen by all its rows.
-template <bool MASKED>
-__device__ __forceinline__ bool needs_mask(const AttnArgs& a, int base, int lo_full, int hi_full) {
-  if constexpr (MASKED) return base + 32 > hi_full || (base < lo_full && base + 32 > a.sinks);
-  return base + 32 > hi_full || base < lo_full;
+// Whether a wave's step of 32 keys needs that mask: [lo_full, hi_full) and the
+// sinks are seen by all its rows. (The plain kernels' conditions stand where
+// they are used: through a function the compiler makes vector code of them, 2%
+// of the time of long chunks.)
+__device__ __forceinline__ bool masked_edge(const AttnArgs& a, int base, int lo_full, int hi_full) {
+  return base + 32 > hi_full || (base < lo_full && base + 32 > a.sinks);
 }
 // Keeps the bytes of those of a quad's tokens that some row of the workgroup sees.
-template <bool MASKED>
-__device__ __forceinline__ uint32_t seen_bytes(const AttnArgs& a, const Stretch& s, int first) {
-  uint32_t m = byte_mask(first, s.lo, s.hi);
-  if constexpr (MASKED) m |= byte_mask(first, 0, a.sinks < s.hi ? (int)a.sinks : s.hi);
-  return m;
+__device__ __forceinline__ uint32_t masked_bytes(const AttnArgs& a, int first, int lo, int hi) {
+  return byte_mask(first, lo, hi) | byte_mask(first, 0, a.sinks < hi ? (int)a.sinks : hi);
 }
 
 template <int RT>

@@ -18,10 +18,10 @@ struct AttnPlan {
   int64_t units;    // row_blocks * B * heads
   int rows;         // of a workgroup
   int row_blocks;   // per (sequence, head), or packed: per head
-  bool packed;      // row blocks by the queries' offsets: attn_first_block
   int chunk;        // keys per split
   int splits;       // most splits of one unit
   int part_floats;  // per (unit, split)
+  bool packed;      // row blocks by the queries' offsets: attn_first_block
 };
 constexpr int attn_tile_max(int dim) { return dim == 64 ? 4 : 2; }  // most row tiles of a wave
 

@@ -55,14 +55,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
   }
   const int split = blockIdx.y;
 
-  // As in kv_attention.hip: page numbers are asked for before the lengths where
-  // they do not depend on them, and the first two tiles before the query rows.
-  Walk<D> walk(a, b, h, a.window > 0 ? 0 : split * (p.chunk / 16), lane);
+  // MASKED: as in kv_attention.hip, page numbers are asked for before the lengths
+  // where they do not depend on them, and the first two tiles before the query
+  // rows (trees are short calls: one of 24 tokens over 4097 keys 25.8 -> 22.3
+  // us). The plain kernel loses by it, 446 -> 458 us for chunks of up to 2047
+  // tokens: its main loop comes out with other registers.
+  Walk<D> walk;
+  if constexpr (MASKED) walk = Walk<D>(a, b, h, a.window > 0 ? 0 : split * (p.chunk / 16), lane);
   const Seq seq = seq_of(a, b, G);
   if ((int64_t)rb * kRows >= seq.rows) return;
   const int row0 = (int)rb * kRows;
   const Stretch all = active_splits<MASKED>(a, p, seq, row0, kRows, G);
-  const int active = all.splits;
+  const int hi_all = all.hi, lo_all = all.lo, active = all.splits;
   if (split >= active) return;
   const int s_first = all.start + split * p.chunk;
   const int s_last = all.end - s_first > p.chunk ? s_first + p.chunk : all.end;
@@ -92,10 +96,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
       walk.step(x == 0 ? 1 : 3);
     }
   };
-  if (tiles > 0) {
-    walk.start(all.key<MASKED>(ahead) >> 4);
-    fetch(fk, fv, ok);
-    fetch(nk, nv, nok);
+  if constexpr (MASKED) {
+    if (tiles > 0) {
+      walk.start(all.key<MASKED>(ahead) >> 4);
+      fetch(fk, fv, ok);
+      fetch(nk, nv, nok);
+    }
   }
 
   Rows<D, RT> r;
@@ -116,9 +122,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
   // a zero probability. `base`: the tile's first place.
   auto clear_v = [&](int base) {
     base = all.key<MASKED>(base + 32 * pair);
-    if (needs_mask<MASKED>(a, base, all.lo, all.hi) || !ok[0] || !ok[1]) {
+    if ((MASKED ? masked_edge(a, base, lo_all, hi_all) : base < lo_all || base + 32 > hi_all) || !ok[0] || !ok[1]) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) fv[x].s &= ok[x] ? seen_bytes<MASKED>(a, all, base + 16 * x + 4 * quad) : 0u;
+      for (int x = 0; x < 2; ++x) fv[x].s &= ok[x] ? (MASKED ? masked_bytes(a, base + 16 * x + 4 * quad, lo_all, hi_all) : byte_mask(base + 16 * x + 4 * quad, lo_all, hi_all)) : 0u;
     }
   };
   // Operand n of the kB that this wave makes of what it fetched: K and V in
@@ -189,7 +195,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
   };
   auto renew = [&](f32x4 (&sc)[RT][2], float (&mx)[RT], int at, uint32_t oks) {
     at = all.key<MASKED>(at);
-    if (needs_mask<MASKED>(a, at, lo_full, hi_full) || oks != 0x101u) {
+    if ((MASKED ? masked_edge(a, at, lo_full, hi_full) : at + 32 > hi_full || at < lo_full) || oks != 0x101u) {
       asm volatile("");  // a branch: most pairs need no mask
       const bool okx[2] = {(oks & 255u) != 0, oks >> 8 != 0};
       if constexpr (MASKED) hide_masked<D, RT>(r, a, seq, sc, at, quad, okx);
@@ -204,13 +210,22 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_kv_attention_tile(Att
     if (lane == 0) page_ok[buf][wave] = ok[half];
   };
   if (tiles > 0) {
+    if constexpr (!MASKED) {
+      walk = Walk<D>(a, b, h, s_first >> 4, lane);
+      walk.start(ahead >> 4);
+      fetch(fk, fv, ok);
+    }
     clear_v(s_first);
     make_tile(0, 0);
-    fk = nk;
+    if constexpr (MASKED) {
+      fk = nk;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      fv[x] = nv[x];
-      ok[x] = nok[x];
+      for (int x = 0; x < 2; ++x) {
+        fv[x] = nv[x];
+        ok[x] = nok[x];
+      }
+    } else {
+      fetch(fk, fv, ok);
     }
     clear_v(s_first + kTile);
     make_tile(1, 1);
