@@ -230,7 +230,8 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, unsigned b, int G) {
 }
 // The sequence and the row block of a unit. Later rows of a sequence see more
 // keys: they come first. Packed blocks' sequence is found by a wave's lanes at
-// once among 64 offsets.
+// once among 64 offsets: the last one before the first that begins behind the
+// block, so that offsets of sequences without rows at the end may be anything.
 struct Block {
   unsigned b, rb;
 };
@@ -242,7 +243,8 @@ __device__ __forceinline__ Block packed_block(const AttnArgs& a, const AttnPlan&
     const int first = a.q_offsets[i];
     // (Offsets are at most T < 2^24, a kv head's rows under 2^31; others are no sequence's.)
     const int64_t s = attn_first_block(first < 0 ? 0 : first, i, G, p.rows);
-    const unsigned before = (unsigned)__popcll(__ballot(b0 + lane < a.B && s <= (int64_t)n));
+    const uint64_t behind = __ballot(b0 + lane >= a.B || s > (int64_t)n);
+    const unsigned before = behind == 0 ? 64u : (unsigned)__builtin_ctzll(behind);
     if (before == 0) break;
     b = (unsigned)b0 + before - 1;
     at = (unsigned)__shfl((int)s, (int)before - 1);

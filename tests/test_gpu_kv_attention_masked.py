@@ -214,6 +214,34 @@ def test_bounds_clamp_trees():
         assert (np.abs(out[:m].double().cpu().numpy() - ro) <= eo).all()
 
 
+@pytest.mark.parametrize("window,sinks", [(0, 0), (90, 9)])
+@pytest.mark.parametrize("lead,B", [(0, 6), (130, 6), (7, 140)])
+def test_ragged_offsets(window, sinks, lead, B):
+    """Row blocks follow the offsets: rows in front of the first sequence and behind the last are left as they were, and
+    offsets of padding sequences at the end may be 0 again."""
+    qs = [2, 0, 64, 1, 70] + [0] * (B - 5)
+    c = Case([200, 30, 300, 1, 90] + [50] * (B - 5), qs, 6, 2, 64, 16, tree=True, seed=12)
+    T = sum(qs)
+    q = torch.cat([c.q[:1].expand(lead, -1, -1), c.q, c.q[:1].expand(40, -1, -1)])
+    off = c.off + lead
+    off[6:] = 0
+    mask = c.mask()
+    mask = torch.cat([mask[:1].expand(lead, -1), mask, mask[:1].expand(40, -1)]).contiguous()
+    first = c.q
+    c.q = q
+    out = torch.full((lead + T + 40, 6, 64), 5.0, device="cuda")
+    lse = torch.full((lead + T + 40, 6), 6.0, device="cuda")
+    c.run(q_offsets=dev(off, torch.int32), max_q=90, tree=mask, window=window, sinks=sinks, out=out, lse=lse)
+    for t, v in ((out, 5), (lse, 6)):
+        assert bool((t[:lead] == v).all()) and bool((t[lead + T:] == v).all())
+    masks = [visible(L, n, window, sinks, s) for L, n, s in zip(c.lens, qs, c.see)]
+    ro, rl, eo, el = attend(first.double().numpy(), c.k, c.v, masks, 64 ** -0.5)
+    assert (np.abs(out[lead:lead + T].double().cpu().numpy() - ro) <= eo).all()
+    got = lse[lead:lead + T].double().cpu().numpy()
+    empty = np.isinf(rl)
+    assert np.array_equal(np.isinf(got), empty) and (np.abs(got[~empty] - rl[~empty]) <= el[~empty]).all()
+
+
 def test_tree_stream_and_graph():
     c = Case([1500, 40, 800], [6, 6, 6], 8, 2, 128, 64, tree=True, seed=9)
     q, table, lens, kg, vg = c.q.cuda(), dev(c.table, torch.int32), dev(c.lens, torch.int32), dev([KG]), dev([VG])
