@@ -57,19 +57,27 @@ __device__ __forceinline__ bool split_last(uint32_t* counter, int active, uint32
 // trips to device scope: partials are asked for together with the statistics.
 // (Splits as a chain of branches: as a loop with a break one token of 64
 // sequences of up to 8192 keys took 78 us, not 68; without branches 69.)
-template <int D, int kRows>
+// PER items of a thread at a time, of at most kJoinHere / PER splits: 32 rows of
+// 128 channels are 4 items a thread, whose trips one after the other were 5.6
+// of the 20 us of a tree of 24 tokens over 4097 keys.
+template <int D, int kRows, int PER>
 __device__ __forceinline__ void join_splits(const AttnArgs& a, const AttnPlan& p, const Seq& seq, unsigned unit, int active,
                                             int row0, int h, int G, float* lds) {
   const float vg = *a.v_g;
   const float* parts = a.part + (int64_t)unit * p.splits * p.part_floats;
   const Rsrc ra = make_rsrc(parts, (uint32_t)(active * p.part_floats * 4));
   const int live = (seq.rows - row0 < kRows ? seq.rows - row0 : kRows) * (D / 4);
-  f32x4 x[kJoinHere];
-  auto load = [&](int n) {  // past the last split or row: zeros, unread
-    const uint32_t at = (uint32_t)(8 * kRows + n * 16);
+  constexpr int kSplits = kJoinHere / PER;
+  f32x4 x[PER][kSplits];
+  auto load = [&](int n0) {  // past the last split or row: zeros, unread
 #pragma unroll
-    for (int s = 0; s < kJoinHere; ++s)
-      x[s] = __builtin_bit_cast(f32x4, bload16_dev(ra, s < active && n < live ? at + (uint32_t)(s * p.part_floats * 4) : kOutOfRange));
+    for (int i = 0; i < PER; ++i) {
+      const int n = n0 + 256 * i;
+      const uint32_t at = (uint32_t)(8 * kRows + n * 16);
+#pragma unroll
+      for (int s = 0; s < kSplits; ++s)
+        x[i][s] = __builtin_bit_cast(f32x4, bload16_dev(ra, s < active && n < live ? at + (uint32_t)(s * p.part_floats * 4) : kOutOfRange));
+    }
   };
   load(threadIdx.x);
   float* jm = lds;  // [active][kRows] m, then l
@@ -80,24 +88,28 @@ __device__ __forceinline__ void join_splits(const AttnArgs& a, const AttnPlan& p
     jl[n] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(ra, (int)at, 4 * kRows, 16));
   }
   __syncthreads();
-  for (int n = threadIdx.x; n < live; n += 256) {
-    const int rr = n / (D / 4), d = n % (D / 4) * 4;
-    float m = kNoKey;
-    for (int s = 0; s < active; ++s) m = __builtin_fmaxf(m, jm[s * kRows + rr]);
-    float l = 0.0f;
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    if (n >= 256) load(n);
-    static_for<kJoinHere>([&](auto step) {
-      constexpr int s = decltype(step)::value;
-      if (s < active) {
-        const float w = __builtin_amdgcn_exp2f(jm[s * kRows + rr] - m);
-        l += w * jl[s * kRows + rr];
-        v += x[s] * w;
-      }
-    });
-    const int64_t orow = out_row(a, seq, row0 + rr, h, G);
-    store4(a, orow * D + d, v * inverse_sum(l, vg));
-    if (d == 0 && a.lse != nullptr) a.lse[orow] = lse_of(m, l);
+  for (int n0 = threadIdx.x; n0 < live; n0 += 256 * PER) {
+    if (n0 >= 256) load(n0);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int n = n0 + 256 * i, rr = n / (D / 4), d = n % (D / 4) * 4;
+      if (PER > 1 && n >= live) break;
+      float m = kNoKey;
+      for (int s = 0; s < active; ++s) m = __builtin_fmaxf(m, jm[s * kRows + rr]);
+      float l = 0.0f;
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      static_for<kSplits>([&](auto step) {
+        constexpr int s = decltype(step)::value;
+        if (s < active) {
+          const float w = __builtin_amdgcn_exp2f(jm[s * kRows + rr] - m);
+          l += w * jl[s * kRows + rr];
+          v += x[i][s] * w;
+        }
+      });
+      const int64_t orow = out_row(a, seq, row0 + rr, h, G);
+      store4(a, orow * D + d, v * inverse_sum(l, vg));
+      if (d == 0 && a.lse != nullptr) a.lse[orow] = lse_of(m, l);
+    }
   }
 }
 #endif
@@ -164,10 +176,15 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
       walk.step(1);
     }
   };
+  // Trees at D 128: records two steps ahead (64 tokens over 4096 keys 26.2 ->
+  // 24.9 us, 16 times over 8192 201 -> 195; with 16 rows 0 to 7% slower, at D 64
+  // no difference, at D 256 no registers).
+  constexpr bool kTwoAhead = MASKED && D == 128 && RT == 2;
   Pair fa, fb;
   if (step0 < step1) {
     walk.start(all.key<MASKED>(ahead) >> 4);
     fetch(fa);
+    if (kTwoAhead && step0 + 1 < step1) fetch(fb);
   }
   Rows<D, RT> r;
   load_rows<D, RT, MASKED>(r, a, seq, row0, h, G, quad, col);
@@ -204,7 +221,20 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
     pv<D, RT, P, 0>(r.o, f.v, vs, pf);
   };
   // The next step's records are on their way while one is computed.
-  if (step0 < step1) {
+  if constexpr (kTwoAhead) {
+    Pair fc;
+    for (int st = step0; st < step1; st += 3) {
+      const int base = s_first + 32 * st;
+      if (st + 2 < step1) fetch(fc);
+      attend(fa, all.key<MASKED>(base));
+      if (st + 1 >= step1) break;
+      if (st + 3 < step1) fetch(fa);
+      attend(fb, all.key<MASKED>(base + 32));
+      if (st + 2 >= step1) break;
+      if (st + 4 < step1) fetch(fb);
+      attend(fc, all.key<MASKED>(base + 64));
+    }
+  } else if (step0 < step1) {
     for (int st = step0; st < step1; st += 2) {
       const int base = s_first + 32 * st;
       if (st + 1 < step1) fetch(fb);
@@ -265,7 +295,10 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArg
   if (active == 1 || p.splits > kJoinHere) return;
   __shared__ uint32_t arrived;
   if (!split_last(a.counters + unit, active, &arrived)) return;
-  join_splits<D, kRows>(a, p, seq, unit, active, row0, h, G, reinterpret_cast<float*>(lds));
+  float* const stats = reinterpret_cast<float*>(lds);
+  if (MASKED && active <= kJoinHere / 4) join_splits<D, kRows, 4>(a, p, seq, unit, active, row0, h, G, stats);
+  else if (MASKED && active <= kJoinHere / 2) join_splits<D, kRows, 2>(a, p, seq, unit, active, row0, h, G, stats);
+  else join_splits<D, kRows, 1>(a, p, seq, unit, active, row0, h, G, stats);
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
