@@ -14,6 +14,12 @@
 // lengths and page numbers, records, partials out, arrival, partials in. So
 // page numbers are asked for before the lengths, records before the query
 // rows, and a step's records while the step before is computed.
+//
+// Sinks and drafted trees are in kernels of their own (MASKED), which walk over
+// the sinks and then the window, and take a mask of 32 bits a row from the
+// tree's words in the few steps that need one. There this kernel also serves
+// up to some hundred rows, where calls are too short for tiles: 16 trees of up
+// to 61 tokens (8 heads of 64 a kv head, window 2000) 31 us, in tiles 47.
 #include "kv_attention_common.h"
 
 namespace nvfp4 {
@@ -391,7 +397,8 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, AttnPlan p) {
 // The rows of a drafted tree's mask from its parents, a thread a row: it walks
 // up its ancestors, whose numbers only fall, so that the words are finished
 // from the last to the first. What bounds it is the chain of LDS reads: a read
-// gives four ancestors.
+// gives four ancestors. 16 trees of up to 61 tokens 3.1 us (4.1 with one), a
+// chain of 4096 302.
 constexpr int kTreeThreads = 256;
 __global__ __launch_bounds__(kTreeThreads) void k_tree_mask(TreeArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)

@@ -467,7 +467,9 @@ __global__ __launch_bounds__(256) void k_kv_write(CacheArgs c, const void* k, co
 }
 
 // The first kv_parts workgroups of a group of tokens write its keys and values,
-// the others turn its queries.
+// the others turn its queries. 8192 tokens of 40 query heads and 8 kv heads of
+// 128 (211 MB) 49 us, 4.3 TB/s, of the 4.7 of a copy; nontemporal stores of the
+// queries 51. One token 4.1 us. Apart, the rotation of the keys is another 34 MB.
 template <int D, bool F32, bool OUT32>
 __global__ __launch_bounds__(256) void k_rope_kv_write(RopeArgs r, RopeUnits units, CacheArgs c, const void* k, const void* v,
                                                        int64_t ks, int64_t vs, const int64_t* slots, const float* kg,
@@ -570,7 +572,11 @@ __device__ __forceinline__ Sums operator+(const Sums& a, const Sums& b) {
 // workgroup goes over the requests for itself (they are few numbers, and read
 // only) and fills its rows; the last to arrive, when nobody reads them any
 // more, writes lengths, the pages that are given back and the pool. So one
-// launch does it all, a step of few rows in one workgroup.
+// launch does it all, a step of few rows in one workgroup. What bounds it is
+// the chain of trips: requests, sums, search, page numbers, rows, arrival. 64
+// requests of 5 rows 3.3 us, 61 prompts of 500000 rows 13 us (their 6 MB take
+// 1.3); with a run of 512 rows a wave, to spare searches, 5.1 and 14, with
+// eight rows of a thread at a time 4.0 and 12.
 template <int N>
 constexpr int kAdvanceRowsOf = 8 * N;  // rows of a workgroup of N threads
 template <int N>
