@@ -76,14 +76,16 @@ extern "C" {
 #define NVFP4_REPACK_PLAIN 0  /* any [R, C] weight, e.g. down_proj */
 #define NVFP4_REPACK_SWIGLU 1 /* merged gate_up [2I, C], rows [gate; up] */
 
-/* Kernel-class override for tests and benchmarks (per calling thread). */
+/* Pairs of channels of a rotation. */
 #define NVFP4_ROPE_HALVES 0     /* channel i turns with i + rotary / 2 */
 #define NVFP4_ROPE_NEIGHBOURS 1 /* channel 2 i turns with 2 i + 1 */
 
-#define NVFP4_POOL_NO_PAGES 1 /* a pool's status: a request found too few free pages, */
+/* Why a pool refused requests. */
+#define NVFP4_POOL_NO_PAGES 1 /* a request found too few free pages, */
 #define NVFP4_POOL_NO_TABLE 2 /* its length passed the block table's width, */
 #define NVFP4_POOL_NO_ROWS 4  /* its rows passed T */
 
+/* Kernel-class override for tests and benchmarks (per calling thread). */
 #define NVFP4_PATH_AUTO 0    /* choose by M */
 #define NVFP4_PATH_GEMV 1    /* decode GEMV sized for M <= 2: W4A4 on the FP4 matrix core with the
                                 blocks kept apart, W4A16 on the vector ALU (any M) */
@@ -561,7 +563,8 @@ int nvfp4_kv_advance(const int32_t* counts, int64_t B, int32_t* seq_lens, int32_
  * a multiple of 8, at most 1024) the first `rotary` channels (a multiple of
  * 16, at most 512) turn in pairs, (i, i + rotary / 2) or (2 i, 2 i + 1) by
  * `pairs`, the others are copied:
- *   angle = positions[axis[i], t] * inv_freq[i] in 64 bits,
+ *   angle = positions[axis[i], t] * inv_freq[i] in 64 bits (below 2^31 quarter
+ *   turns, which no position passes with frequencies up to 1),
  *   c = fl(factor * cos(angle)), s = fl(factor * sin(angle)) in fp32,
  *   (x, y) -> (fl(fl(x c) - fl(y s)), fl(fl(y c) + fl(x s))), rounded to out_dtype.
  * positions: device int32 [axes, T] (1 to 16 axes: time, height, width of a

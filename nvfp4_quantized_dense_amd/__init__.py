@@ -774,6 +774,8 @@ def nvfp4_tree_mask(parents, q_offsets, max_q, positions=None, tree=None, stream
     T = _list(parents, "parents", torch.int32).numel()
     if q_offsets is None:
         B = T // max_q if max_q > 0 else 0
+        if T != B * max_q:
+            raise ValueError("without q_offsets parents must have max_q elements a sequence")
     else:
         B = _list(q_offsets, "q_offsets", torch.int32).numel() - 1
     if tree is None:
@@ -845,8 +847,6 @@ def nvfp4_kv_attention(q, cache, block_table, seq_lens, k_g, v_g, q_offsets=None
         if len(tree.shape) != 2 or _list(tree, "tree", torch.int64).shape[0] != T or tree.shape[1] < 1:
             raise ValueError(f"tree must be int64 [{T}, words]")
         words = tree.shape[1]
-        if not tree.is_cuda:
-            _not_on_gpu()
     kg, vg = _scalar(k_g, "k_g"), _scalar(v_g, "v_g")
     if ws is not None and not ws.is_contiguous():
         raise ValueError("ws must be contiguous")
@@ -860,6 +860,7 @@ def nvfp4_kv_attention(q, cache, block_table, seq_lens, k_g, v_g, q_offsets=None
             ws = torch.empty(max(n, ATTENTION_COUNTER_BYTES), dtype=torch.uint8, device=q.device)
             ws[:ATTENTION_COUNTER_BYTES].zero_()
     if sinks or tree is not None:
+        _same_gpu(q, cache, block_table, seq_lens, k_g, v_g, q_offsets, tree, out, lse, ws)
         _check("nvfp4_kv_attention_masked",
                lib().nvfp4_kv_attention_masked(q.data_ptr(), qs, T, B, heads_q, _ptr(q_offsets), max_q, cache.data_ptr(), pages,
                                                page_size, heads, dim, block_table.data_ptr(), table_stride if B > 1 else width,

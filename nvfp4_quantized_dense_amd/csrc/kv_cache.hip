@@ -554,7 +554,6 @@ __global__ __launch_bounds__(256) void k_kv_pool_reset(int32_t* pool, int64_t pa
     pool[i] = i == 0 ? (int32_t)pages : i < kPoolHead ? 0 : (int32_t)(pages - 1 - (i - kPoolHead));
 }
 
-
 // Sums of a request's rows, pages taken and pages given back. They stop at
 // 2^30: past T, the pool and a table's width nothing depends on their value.
 struct Sums {

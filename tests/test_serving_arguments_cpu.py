@@ -170,6 +170,22 @@ def test_another_gpu_is_refused(monkeypatch):
                       out=t(3, 4, 64, dtype=BF16).as_subclass(OnGpu))
 
 
+def test_attention_on_another_gpu_is_refused(monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    cache, g, q = nv.nvfp4_kv_cache(2, 16, 2, 64).as_subclass(OnGpu), torch.ones(1).as_subclass(OnGpu), t(3, 4, 64, dtype=BF16).as_subclass(OnGpu)
+    for kw in dict(sinks=4, window=8, lse=t(12, dtype=torch.float32).as_subclass(OnOther)), dict(tree=t(3, 1, dtype=I64).as_subclass(OnOther)):
+        with pytest.raises(ValueError, match="current GPU, cuda:0"):
+            nv.nvfp4_kv_attention(q, cache, t(3, 2).as_subclass(OnGpu), t(3).as_subclass(OnGpu), g, g, out=torch.empty_like(q),
+                                  ws=torch.zeros(1 << 20, dtype=torch.uint8).as_subclass(OnGpu), **kw)
+
+
+@pytest.mark.parametrize("T,max_q", [(3, 5), (3, 0), (7, 2)])
+def test_tree_mask_of_odd_lengths_is_refused(T, max_q):
+    """Without offsets: not a mask that nothing has been written to."""
+    with pytest.raises(ValueError, match="max_q elements a sequence"):
+        nv.nvfp4_tree_mask(t(T), None, max_q)
+
+
 @pytest.fixture(scope="module")
 def scan(tmp_path_factory):
     so = str(tmp_path_factory.mktemp("plan") / "plan.so")
