@@ -573,14 +573,12 @@ __device__ __forceinline__ Sums operator+(const Sums& a, const Sums& b) {
 // more, writes lengths, the pages that are given back and the pool. So one
 // launch does it all, a step of few rows in one workgroup. What bounds it is
 // the chain of trips: requests, sums, search, page numbers, rows, arrival. 64
-// requests of 5 rows 3.3 us, 61 prompts of 500000 rows 13 us (their 6 MB take
+// requests of 5 rows 3.3 us, 61 prompts of 500000 rows 12.5 us (their 6 MB take
 // 1.3); with a run of 512 rows a wave, to spare searches, 5.1 and 14, with
-// eight rows of a thread at a time 4.0 and 12.
-template <int N>
-constexpr int kAdvanceRowsOf = 8 * N;  // rows of a workgroup of N threads
-template <int N>
+// eight rows of a thread at a time 4.0 and 12. ROWS: rows of a thread, N threads.
+template <int N, int ROWS>
 __global__ __launch_bounds__(N) void k_kv_advance(AdvanceArgs a, Div page) {
-  constexpr int kAdvanceThreads = N, kAdvanceRows = kAdvanceRowsOf<N>;
+  constexpr int kAdvanceThreads = N, kAdvanceRows = ROWS * N;
   __shared__ Sums waves[kAdvanceThreads / 64];
   __shared__ uint32_t end[kAdvanceThreads], begin[kAdvanceThreads], before[kAdvanceThreads], given_end[kAdvanceThreads];
   __shared__ int old[kAdvanceThreads], held[kAdvanceThreads], first_gone[kAdvanceThreads];
@@ -650,13 +648,15 @@ __global__ __launch_bounds__(N) void k_kv_advance(AdvanceArgs a, Div page) {
     __syncthreads();
     return q;
   };
-  // The first of the chunk's requests whose sum passes n.
-  auto find = [&](const uint32_t* sums, uint32_t n) {
-    int lo = 0;
+  // The first of the chunk's requests whose sum passes each n.
+  auto find = [&](const uint32_t* sums, const auto& n, auto& i) {
+    constexpr int kOf = sizeof(n) / sizeof(n[0]);
+#pragma unroll
+    for (int u = 0; u < kOf; ++u) i[u] = 0;
 #pragma unroll
     for (int d = kAdvanceThreads / 2; d > 0; d /= 2)
-      if (sums[lo + d - 1] <= n) lo += d;
-    return lo;
+#pragma unroll
+      for (int u = 0; u < kOf; ++u) i[u] += sums[i[u] + d - 1] <= n[u] ? d : 0;
   };
 
   const int64_t chunks = (a.B + kAdvanceThreads - 1) / kAdvanceThreads;
@@ -670,25 +670,18 @@ __global__ __launch_bounds__(N) void k_kv_advance(AdvanceArgs a, Div page) {
     const uint32_t from = sum.rows;
     mine = sweep(chunk, sum);
     const uint32_t to = sum.rows < row1 ? sum.rows : row1;
-    // Four rows of a thread at a time without a branch, so that their searches
-    // and their page numbers are on their way together.
-    constexpr int kRows = 4;
-    for (uint32_t t0 = (from > row0 ? from : row0) + tid; t0 < to; t0 += kRows * kAdvanceThreads) {
-      uint32_t t[kRows];
-      int i[kRows], position[kRows], p[kRows], in[kRows], shift[kRows];
-      int32_t* entry[kRows];
-      bool live[kRows], comes[kRows];
+    // A thread's rows without a branch, so that their searches and their page
+    // numbers are on their way together.
+    for (uint32_t t0 = (from > row0 ? from : row0) + tid; t0 < to; t0 += ROWS * kAdvanceThreads) {
+      uint32_t t[ROWS];
+      int i[ROWS], position[ROWS], p[ROWS], in[ROWS], shift[ROWS];
+      int32_t* entry[ROWS];
+      bool live[ROWS], comes[ROWS];
 #pragma unroll
-      for (int u = 0; u < kRows; ++u) {
-        t[u] = t0 + u * kAdvanceThreads;
-        i[u] = 0;
-      }
+      for (int u = 0; u < ROWS; ++u) t[u] = t0 + u * kAdvanceThreads;
+      find(end, t, i);
 #pragma unroll
-      for (int d = kAdvanceThreads / 2; d > 0; d /= 2)
-#pragma unroll
-        for (int u = 0; u < kRows; ++u) i[u] += end[i[u] + d - 1] <= t[u] ? d : 0;
-#pragma unroll
-      for (int u = 0; u < kRows; ++u) {
+      for (int u = 0; u < ROWS; ++u) {
         const int was = old[i[u]];
         live[u] = t[u] < to && was >= 0;
         const int pos = live[u] ? was + (int)(t[u] - begin[i[u]]) : 0, col = (int)div_n((uint32_t)pos, page);
@@ -702,7 +695,7 @@ __global__ __launch_bounds__(N) void k_kv_advance(AdvanceArgs a, Div page) {
         shift[u] = a.offsets != nullptr ? a.offsets[b] : 0;
       }
 #pragma unroll
-      for (int u = 0; u < kRows; ++u) {
+      for (int u = 0; u < ROWS; ++u) {
         if (t[u] >= to) continue;
         if (comes[u] && in[u] == 0) *entry[u] = p[u];
         if (a.slots != nullptr) a.slots[t[u]] = live[u] ? (int64_t)p[u] * page.d + in[u] : -1;
@@ -723,6 +716,36 @@ __global__ __launch_bounds__(N) void k_kv_advance(AdvanceArgs a, Div page) {
   const int64_t left64 = (int64_t)top - popped + sum.given;
   const int left = left64 < a.pages ? (int)left64 : a.pages;
   sum = {0, 0, 0};
+  // Pages of a chunk's requests from sum `from` on come back so that a growth
+  // that is undone leaves the stack as it was; `of` of a thread at a time
+  // (7800 pages one by one 22 us, by eight 12; few of them by eight 1 us more).
+  auto back = [&](uint32_t from, int64_t chunk, auto of) {
+    constexpr int kOf = decltype(of)::value;
+    for (uint32_t j0 = from + tid; j0 < sum.given; j0 += kOf * kAdvanceThreads) {
+      uint32_t j[kOf];
+      int i[kOf], p[kOf];
+      int32_t* entry[kOf];
+#pragma unroll
+      for (int u = 0; u < kOf; ++u) {
+        const uint32_t n = j0 + u * kAdvanceThreads;
+        j[u] = n < sum.given ? n : j0;
+      }
+      find(given_end, j, i);
+#pragma unroll
+      for (int u = 0; u < kOf; ++u) {
+        const uint32_t i0 = i[u] > 0 ? given_end[i[u] - 1] : from;
+        entry[u] = a.table + (chunk * kAdvanceThreads + i[u]) * a.table_stride + first_gone[i[u]] + (j[u] - i0);
+        p[u] = *entry[u];
+      }
+#pragma unroll
+      for (int u = 0; u < kOf; ++u) {
+        if (u > 0 && j[u] == j0) break;
+        const int at = left - 1 - (int)j[u];
+        if (at >= 0) stack[at] = p[u];
+        *entry[u] = -1;
+      }
+    }
+  };
   ask(0);
   for (int64_t chunk = 0; chunk < chunks; ++chunk) {
     const uint32_t from = sum.given;
@@ -733,15 +756,8 @@ __global__ __launch_bounds__(N) void k_kv_advance(AdvanceArgs a, Div page) {
       a.seq_lens[b] = mine.len;
       if (a.q_offsets != nullptr) a.q_offsets[b + 1] = (int32_t)(end[tid] < T ? end[tid] : T);
     }
-    // Pages come back so that a growth that is undone leaves the stack as it was.
-    for (uint32_t j = from + tid; j < sum.given; j += kAdvanceThreads) {
-      const int i = find(given_end, j);
-      const uint32_t i0 = i > 0 ? given_end[i - 1] : from;
-      int32_t* entry = a.table + (chunk * kAdvanceThreads + i) * a.table_stride + first_gone[i] + (j - i0);
-      const int at = left - 1 - (int)j;
-      if (at >= 0) stack[at] = *entry;
-      *entry = -1;
-    }
+    if (sum.given - from > 4 * kAdvanceThreads) back(from, chunk, std::integral_constant<int, 8>{});
+    else back(from, chunk, std::integral_constant<int, 1>{});
   }
   if (tid == 0) {
     if (a.q_offsets != nullptr) a.q_offsets[0] = 0;
@@ -839,8 +855,12 @@ hipError_t launch_kv_pool_reset(int32_t* pool, int64_t pages, hipStream_t s) {
 hipError_t launch_kv_advance(const AdvanceArgs& a, hipStream_t s) {
   const Div page = div_by((uint32_t)a.page_size);
   auto groups = [&](int rows) { return dim3((unsigned)(a.T > rows ? (a.T + rows - 1) / rows : 1)); };
-  if (a.B <= 256) k_kv_advance<256><<<groups(kAdvanceRowsOf<256>), dim3(256), 0, s>>>(a, page);
-  else k_kv_advance<1024><<<groups(kAdvanceRowsOf<1024>), dim3(1024), 0, s>>>(a, page);
+  // Many rows of a workgroup where there would be many workgroups, whose
+  // arrivals queue: 512 threads of 4 / 256 of 2, 500000 rows and back 22.5 /
+  // 29 us, 32000 11 / 10.3; and a chunk for as many requests as there are.
+  if (a.B <= 256 && a.T <= 1 << 17) k_kv_advance<256, 2><<<groups(512), dim3(256), 0, s>>>(a, page);
+  else if (a.B <= 512) k_kv_advance<512, 4><<<groups(2048), dim3(512), 0, s>>>(a, page);
+  else k_kv_advance<1024, 2><<<groups(2048), dim3(1024), 0, s>>>(a, page);
   return hipGetLastError();
 }
 

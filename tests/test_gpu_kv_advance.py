@@ -70,6 +70,23 @@ def test_rows_of_many_workgroups(B, most, page):
     assert len(ref.stack) == B * width
 
 
+@pytest.mark.parametrize("B,most,page", [(40, 8000, 16), (256, 1100, 16), (500, 600, 32), (1500, 200, 16)])
+def test_many_rows_and_pages_come_and_go(B, most, page):
+    """More than 2^17 rows, requests of more than one chunk, thousands of pages taken and given back in one call."""
+    r = np.random.RandomState(B)
+    width = -(-most // page)
+    ref = Pages([0] * B, width, page, B * width, seed=B)
+    side = Side(ref)
+    counts = r.randint(most // 2, most + 1, B)
+    side.step(counts, int(counts.sum()))
+    gone = np.where(r.rand(B) < 0.6, r.randint(1, most // 2, B), 0)
+    side.step(-gone, 0)
+    back = np.where(r.rand(B) < 0.5, gone, -most)
+    side.step(back, int(np.maximum(back, 0).sum()) + 7)
+    side.step(np.full(B, -most), 3)
+    assert ref.status == 0 and len(ref.stack) == B * width
+
+
 def test_undone_growth_leaves_the_pool():
     ref = Pages([5, 31, 0, 100], 20, 16, 50, seed=3)
     side = Side(ref)
