@@ -570,7 +570,7 @@ int nvfp4_kv_advance(const int32_t* counts, int64_t B, int32_t* seq_lens, int32_
  * positions: device int32 [axes, T] (1 to 16 axes: time, height, width of a
  * picture's tokens; axis stride in elements, 0 if all are alike); axis: device
  * int32 [rotary / 2], the axis of each frequency (an axis outside the
- * positions turns nothing), NULL: axis 0; inv_freq: device fp32 [rotary / 2].
+ * positions turns nothing: c = 1, s = 0, without factor), NULL: axis 0; inv_freq: device fp32 [rotary / 2].
  * out may be x (one type and stride), not overlap it otherwise. With
  * -inv_freq it is the inverse, and the gradient of the rotation.
  */

@@ -244,10 +244,12 @@ __device__ __forceinline__ void rope_table(const RopeArgs& r, int64_t first, int
   for (int n = threadIdx.x; n < tokens * (int)half.d; n += 256) {
     const int t = (int)(((uint64_t)(uint32_t)n * half.m) >> half.shift), i = n - t * (int)half.d;
     const int axis = r.axis != nullptr ? r.axis[i] : 0;
-    const int pos = (unsigned)axis < (unsigned)r.axes ? r.positions[axis * r.axis_stride + first + t] : 0;
+    const bool turns = (unsigned)axis < (unsigned)r.axes;
+    const double angle = turns ? (double)r.positions[axis * r.axis_stride + first + t] * (double)r.inv_freq[i] : 0.0;
     double c, s;
-    cos_sin((double)pos * (double)r.inv_freq[i], c, s);
-    table[n] = f32x2{(float)(r.factor * c), (float)(r.factor * s)};
+    cos_sin(angle, c, s);
+    const double factor = turns ? r.factor : 1.0;  // what is not turned stays as it is
+    table[n] = f32x2{(float)(factor * c), (float)(factor * s)};
   }
 }
 
