@@ -69,8 +69,8 @@ class DecoderLayer:
         return self.ws
 
     def __call__(self, x, residual, slots, block_table, seq_lens, q_offsets, max_q, max_len, trace=None, positions=None, tree=None):
-        """x, residual bf16 [T, hidden] (residual is updated in place) -> bf16 [T, hidden]. positions int32 [T] or
-        [axes, T], where the layer turns; tree: the queries are drafted trees."""
+        """x, residual bf16 [T, hidden] (residual is updated in place) -> bf16 [T, hidden]. positions int32 [axes, T]
+        or [T], of all axes, where the layer turns; tree: the queries are drafted trees."""
         T, Hq, H, D = x.shape[0], self.heads_q, self.heads, self.dim
         codes, scales, residual, row_g = nv.add_rmsnorm_nvfp4_quant_per_token(x, self.norm1, residual=residual,
                                                                                residual_out=residual)

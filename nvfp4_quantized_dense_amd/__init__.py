@@ -23,6 +23,7 @@ DTYPE_BF16, DTYPE_F32 = 0, 1
 MODE_W4A4, MODE_W4A16, MODE_W4A4_DYN, MODE_W4A16_AWQ = 0, 1, 2, 3
 REPACK_PLAIN, REPACK_SWIGLU = 0, 1
 ROPE_HALVES, ROPE_NEIGHBOURS = 0, 1
+ROPE_AXES = 16  # at most
 POOL_NO_PAGES, POOL_NO_TABLE, POOL_NO_ROWS = 1, 2, 4
 PATH_AUTO, PATH_GEMV, PATH_STREAM, PATH_TILED, PATH_TILED64, PATH_MID = 0, 1, 2, 3, 4, 5
 
@@ -713,13 +714,16 @@ def _rope_plan(positions, inv_freq, axes, T, dim):
     shape = positions.shape
     if positions.dtype is not torch.int32 or len(shape) not in (1, 2) or shape[-1] != T or (T > 1 and positions.stride(-1) != 1):
         raise ValueError(f"positions must be int32 [{T}] or [axes, {T}], each axis dense")
-    return (0, 1, 2 * n) if len(shape) == 1 else (positions.stride(0) if shape[0] > 1 else 0, shape[0], 2 * n)
+    if len(shape) == 1:  # of all axes alike
+        return 0, 1 if axes is None else ROPE_AXES, 2 * n
+    return positions.stride(0) if shape[0] > 1 else 0, shape[0], 2 * n
 
 
 def nvfp4_rope(x, positions, inv_freq, axes=None, pairs=ROPE_HALVES, factor=1.0, out=None, out_dtype=None, stream=None):
-    """x [T, heads, head_dim] (bf16 or f32, token stride free) turned by its positions (int32 [T] or [axes, T]): frequency i of
-    inv_freq (fp32 [rotary / 2]) with the positions of axis axes[i] (int32 [rotary / 2]; None: the first), cosine and sine
-    times factor, channels paired by `pairs`. Returns out (x's type by default; may be x)."""
+    """x [T, heads, head_dim] (bf16 or f32, token stride free) turned by its positions (int32 [axes, T], or [T]: of all axes):
+    frequency i of inv_freq (fp32 [rotary / 2]) with the positions of axis axes[i] (int32 [rotary / 2]; None: the first),
+    cosine and sine times factor, channels paired by `pairs`. Frequencies of an axis below 0 or past the positions' (16 of
+    [T]) turn nothing. Returns out (x's type by default; may be x)."""
     shape = x.shape
     if len(shape) != 3:
         raise ValueError("x must be [tokens, heads, head_dim]")
