@@ -130,7 +130,7 @@ class Batch:
 
 class DeviceBatch:
     """Sequences whose lengths, block tables and pool of pages stay on the GPU: nothing of a step depends on the host but
-    its number of rows, and a refused sequence is seen in `status`."""
+    its number of rows. A refusal is seen in `status`, whose it is in the slots of its rows, -1."""
 
     def __init__(self, layer, sequences, max_len):
         self.layer, self.max_len, dev = layer, max_len, layer.cache.device
@@ -151,16 +151,20 @@ class DeviceBatch:
 
     def accept(self, call, kept, counts, dropped):
         """After a drafted call: its rows `kept` (int64, each sequence's accepted ones in order, counts[b] of them) become
-        the sequence's next tokens, and dropped[b] = tokens drafted - counts[b] are taken back."""
-        layer = self.layer
-        k, v = nv.nvfp4_kv_read(layer.cache, call["slots"][kept], layer.kv_g, layer.kv_g, dtype=torch.float32)
+        the sequence's next tokens, and dropped[b] = tokens drafted - counts[b] are taken back. A sequence whose draft was
+        refused holds none of it (its rows have no slot) and stays as it is."""
+        layer, slots = self.layer, call["slots"]
+        if slots.numel() == 0:
+            return
+        k, v = nv.nvfp4_kv_read(layer.cache, slots[kept], layer.kv_g, layer.kv_g, dtype=torch.float32)
         first = call["q_offsets"][:-1].long()
         place = torch.arange(kept.numel(), device=kept.device)
         begin = torch.cumsum(counts, 0) - counts
         seq = torch.repeat_interleave(counts.long(), output_size=kept.numel())
-        to = call["slots"][first[seq] + place - begin[seq]]
+        to = slots[first[seq] + place - begin[seq]]
         nv.nvfp4_kv_write(k, v, to, layer.kv_g_inv, layer.kv_g_inv, layer.cache)
-        nv.nvfp4_kv_advance(-dropped, self.lens, self.table, self.pool, layer.page_size, 0)
+        came = (first < call["q_offsets"][1:]) & (slots[first.clamp(max=slots.numel() - 1)] >= 0)
+        nv.nvfp4_kv_advance(-dropped * came, self.lens, self.table, self.pool, layer.page_size, 0)
 
 
 def main():
