@@ -120,13 +120,16 @@ __device__ __forceinline__ void join_splits(const AttnArgs& a, const AttnPlan& p
 }
 #endif
 
-// Workgroups per CU that the registers are held to.
-template <int D, int RT>
-constexpr int kAttnWgs = D == 256 ? 3 - RT : RT == 2 ? 2 : D == 64 ? 4 : 3;
+// Workgroups per CU that the registers are held to. 16 plain rows of 64
+// channels: five, as 1280 units are one round of the chip so: 160 sequences of
+// up to 2048 keys on 8 heads 31.5 us, 35.3 with four (bound 4 gave 98 registers,
+// 2 too many); of 200 sequences of up to 3000 keys, f32, 64.8 and 62.7.
+template <int D, int RT, bool MASKED>
+constexpr int kAttnWgs = D == 256 ? 3 - RT : RT == 2 ? 2 : D == 64 ? (MASKED ? 4 : 5) : 3;
 
 // P: f16 parts of a probability. MASKED: sinks or a tree mask.
 template <int D, int RT, int P, bool MASKED>
-__global__ __launch_bounds__(256, (kAttnWgs<D, RT>)) void k_kv_attention(AttnArgs a, AttnPlan p) {
+__global__ __launch_bounds__(256, (kAttnWgs<D, RT, MASKED>)) void k_kv_attention(AttnArgs a, AttnPlan p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int kB = D / 16, kW = D / 32, kRows = 16 * RT;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
