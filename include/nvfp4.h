@@ -622,6 +622,8 @@ int nvfp4_tree_mask(const int32_t* parents, int64_t T, int64_t B, const int32_t*
  * ignored; if a sequence has more than max_q queries, keys of the ones past
  * max_q are hidden. tree_words: ceil(max_q / 64) to 64. A window must be at
  * least max_q, so that it hides no drafted key. Workspace as above.
+ * A key that a query does not see has no part in its results, whatever the cache
+ * holds of it (a token that was never written, values that are NaN).
  */
 int nvfp4_kv_attention_masked(const uint16_t* q, int64_t q_stride, int64_t T, int64_t B, int64_t heads_q,
                               const int32_t* q_offsets, int64_t max_q, const void* cache, int64_t pages, int64_t page_size,

@@ -195,6 +195,8 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT, MASKED>)) void k_kv_attention
     fetch(fa);
     if (kTwoAhead && step0 + 1 < step1) fetch(fb);
   }
+  __shared__ uint32_t no_number[4][kB], nan_rows[4][kRows];  // MASKED: by wave
+  if (MASKED && lane < kRows) nan_rows[wave][lane] = 0;
   Rows<D, RT> r;
   load_rows<D, RT, MASKED>(r, a, seq, row0, h, G, quad, col);
   auto attend = [&](Pair& f, int base) {
@@ -214,12 +216,18 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT, MASKED>)) void k_kv_attention
     }
     if (edge) {
       asm volatile("");  // a branch: most steps need no mask
-      if constexpr (MASKED) hide_masked<D, RT>(r, a, seq, sc, base, quad, f.ok);
-      else hide_scores<D, RT>(r, sc, base, quad, f.ok);
+      if constexpr (!MASKED) hide_scores<D, RT>(r, sc, base, quad, f.ok);
       // Tokens no row sees may never have been written: their V scales
       // become zero, so that no NaN code meets a zero probability.
 #pragma unroll
       for (int x = 0; x < 2; ++x) f.v[x].s &= f.ok[x] ? (MASKED ? masked_bytes(a, base + 16 * x + 4 * quad, all.lo, all.hi) : byte_mask(base + 16 * x + 4 * quad, all.lo, all.hi)) : 0u;
+      if constexpr (MASKED) {
+        const bool nans = any_nan(f.v);
+        if (nans) take_nans(f.v, lane, no_number[wave]);
+        hide_masked<D, RT>(r, a, seq, sc, base, quad, f.ok, [&](int t, uint32_t see) {
+          if (nans) note_nans<D>(nan_rows[wave] + 16 * t, lane, see, no_number[wave], true, true);
+        });
+      }
     }
     f16x8 pf[P][RT];
     float mx[RT];
@@ -286,8 +294,9 @@ __global__ __launch_bounds__(256, (kAttnWgs<D, RT, MASKED>)) void k_kv_attention
     // channels 16 y + 4 quad + [0, 4) of row 16 t + col.
     const bool live = row0 + rr < seq.rows;
     const int64_t orow = out_row(a, seq, row0 + rr, h, G);
+    const uint32_t bad = MASKED ? nan_rows[0][rr] | nan_rows[1][rr] | nan_rows[2][rr] | nan_rows[3][rr] : 0u;
     for (int y = wave; y < kB; y += 4) {
-      const f32x4 v = wo(0, y) + wo(1, y) + wo(2, y) + wo(3, y);
+      const f32x4 v = nan_if(bad >> y & 1u, wo(0, y) + wo(1, y) + wo(2, y) + wo(3, y));
       if (!live) continue;
       if (active == 1) store4(a, orow * D + 16 * y + 4 * quad, v * inverse_sum(l, vg));
       else bstore16_dev(rp, (uint32_t)(8 * kRows + (rr * D + 16 * y + 4 * quad) * 4), __builtin_bit_cast(u32x4, v));

@@ -436,21 +436,69 @@ __device__ __forceinline__ void hide_scores(const Rows<D, RT>& r, f32x4 (&sc)[RT
   }
 }
 
-// The same where sinks or a tree decide, a bit a key.
-template <int D, int RT>
+// The same where sinks or a tree decide. seen(t, bits): the keys that row `col`
+// of tile t sees, a bit each.
+template <int D, int RT, class F>
 __device__ __forceinline__ void hide_masked(const Rows<D, RT>& r, const AttnArgs& a, const Seq& seq, f32x4 (&sc)[RT][2], int base,
-                                            int quad, const bool (&ok)[2]) {
+                                            int quad, const bool (&ok)[2], F&& seen) {
   const uint32_t sinks = low_bits((int)a.sinks - base), pages = (ok[0] ? 0xFFFFu : 0u) | (ok[1] ? 0xFFFF0000u : 0u);
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     uint32_t see = low_bits(r.lo[t] + r.n[t] - base) & (~low_bits(r.lo[t] - base) | sinks) & pages;
     if (a.tree != nullptr && see != 0) see &= tree_bits(a, r.row[t], base - (int)((int64_t)seq.len - seq.nq));
+    seen(t, see);
     see >>= 4 * quad;
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int e = 0; e < 4; ++e) sc[t][x][e] = see & (1u << (16 * x + e)) ? sc[t][x][e] : -__builtin_inff();
   }
+}
+
+// Values that are not numbers in a step that some rows see a part of: a hidden
+// key's probability is 0, but 0 times NaN is not. (A rejected branch may hold
+// them, or padding of a draft that was never written.) So their scales become
+// zero, and the rows that see such a value are noted, whose outputs become NaN
+// in its channels at the end. An E4M3 scale is NaN, with either sign, if its
+// seven low bits are set. It costs one token of 30001 keys behind a window 9.6
+// -> 9.8 us, a tree of 24 over 4097 keys 17.1 -> 17.3.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t s) { return ((s & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+template <int D, int PARTS>
+__device__ __forceinline__ bool any_nan(const VFrag<D, PARTS> (&v)[2]) {
+  return __builtin_expect(__any((nan_bytes(v[0].s) | nan_bytes(v[1].s)) != 0), 0);
+}
+// For rare steps: what the compiler would compute of the lane's number before
+// the loop, it would hold in registers all through it.
+__device__ __forceinline__ int lane_here(int lane) {
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+// Clears them, and notes in blocks[] which of the pair's 32 tokens had one.
+template <int D, int PARTS>
+__device__ __forceinline__ void take_nans(VFrag<D, PARTS> (&v)[2], int lane, uint32_t* blocks) {
+  constexpr int kN = D / 16 / PARTS;
+  lane = lane_here(lane);
+  if (lane < kN) blocks[lane] = 0;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const uint32_t z = nan_bytes(v[x].s) >> 7;  // a 1 in each such byte, and side by side
+    atomicOr(blocks + (lane & (kN - 1)), ((z * 0x01020408u) >> 24 & 15u) << (16 * x + 4 * (lane >> 4)));
+    v[x].s &= ~(z * 255u);
+  }
+}
+// Notes in `rows`, a tile's, a bit for each channel block of which the row sees
+// such a value: tokens `see`, and blocks[] as above, of its first and second
+// half where those are given. (The four lanes of a row write the same.)
+template <int D>
+__device__ __forceinline__ void note_nans(uint32_t* rows, int lane, uint32_t see, const uint32_t* blocks, bool first, bool second) {
+  uint32_t noted = 0;
+#pragma unroll 1
+  for (int y = first ? 0 : D / 32; y < (second ? D / 16 : D / 32); ++y) noted |= see & blocks[y] ? 1u << y : 0u;
+  rows[lane_here(lane) & 15] |= noted;
+}
+__device__ __forceinline__ f32x4 nan_if(bool yes, const f32x4& v) {
+  const float n = __builtin_nanf("");
+  return yes ? f32x4{n, n, n, n} : v;
 }
 
 // Whether a wave's step of 32 keys needs that mask: [lo_full, hi_full) and the
