@@ -610,8 +610,9 @@ int nvfp4_tree_mask(const int32_t* parents, int64_t T, int64_t B, const int32_t*
  * nvfp4_kv_attention with a window that keeps the first keys, and for drafted
  * trees. With a window (window > 0) the keys 0 .. sinks - 1 stay visible to
  * every query at or behind them: the query at p sees j <= p with j < sinks or
- * j > p - window. Keys between the two stretches are not read, nor are the
- * table's entries of pages that lie between them whole.
+ * j > p - window. The table's entries of pages that lie whole
+ * between the two stretches may hold anything (both are walked over in steps of
+ * 32 keys, so some of what lies between may be read).
  * tree (device, [T, tree_words], 8-byte aligned; NULL: causal): the n queries
  * of a sequence are drafted tokens whose keys are its last n, n <= max_q <=
  * 4096. Bit d % 64 of word d / 64 of a query's row says whether it sees the
