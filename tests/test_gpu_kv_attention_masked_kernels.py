@@ -91,6 +91,16 @@ def test_kernel(pick, D, tree, kind, H, G, B, q, L, window, sinks, T):
     c.verify(window, sinks, out_dtype=torch.bfloat16, **kw)
 
 
+@pytest.mark.parametrize("D,G", [(64, 300), (128, 257), (256, 130)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_many_heads_of_a_group(D, G, tree):
+    """Row blocks within one query, and across the next."""
+    c = made(D, 1, G, 3, 5, 200, 11, tree, seed=3, P=16)
+    c.verify(50, 9)
+    if tree:
+        c.verify()
+
+
 @pytest.mark.parametrize("D,tree,H,G,B,q,L,window,sinks", [(64, True, 2, 4, 2, 4, 700, 0, 0), (64, False, 1, 8, 2, 20, 400, 90, 5), (128, True, 1, 5, 1, 24, 1500, 0, 0),
                                                            (128, True, 1, 25, 1, 3, 400, 60, 9), (128, False, 1, 9, 1, 10, 500, 200, 40),
                                                            (256, True, 1, 2, 2, 7, 300, 0, 0), (256, False, 1, 3, 2, 40, 300, 100, 3), (256, True, 2, 17, 1, 4, 900, 0, 0)])
